@@ -61,6 +61,8 @@ typedef enum {
 
 enum { QMOE_Q2 = 2, QMOE_Q4 = 4 };        /* block formats (bits per code) */
 enum { QMOE_F32 = 0, QMOE_BF16 = 1 };     /* activation dtypes */
+enum { QMOE_I8 = 2 };                     /* signed 8-bit codes with scales (qmoe_linear operands) */
+enum { QMOE_ACT_NONE = 0, QMOE_ACT_RELU = 1, QMOE_ACT_SILU = 2, QMOE_ACT_GELU = 3 }; /* qmoe_linear */
 enum { QMOE_GATE_UP = 0, QMOE_DOWN = 1 }; /* packed matrix kinds */
 
 /* One layer's experts, already packed by qmoe_pack().
@@ -376,6 +378,89 @@ qmoe_status qmoe_stack_decode_host(qmoe_stack *stack, const float *x_host, float
 qmoe_status qmoe_ngram_gather(const int32_t *ngrams, int T, uint64_t seed, const uint8_t *codes,
                               const uint16_t *scales, int64_t R, int D, float *out, int32_t *rows,
                               qmoe_stream_t stream);
+
+/* ------------------------------------------- residual norm, 8-bit output --
+ * The step from a residual stream to the operand of an 8-bit (or bf16) dense
+ * product. This entry point and the three below it have no counterpart in the
+ * method's sources: they are the dense half of a decode step (final norm,
+ * dense product, next token), which a user of the routed half needs beside it.
+ *   z = x_in[t,:] + y[t,:]                  (fp32, one rounding; y NULL: z = x_in)
+ *   r = 1 / sqrt(mean(z^2) + eps),  p = z * gain    (gain NULL: p = z)
+ *   z_out    = z in `dtype`                 (the updated residual stream)
+ *   norm_out = p * r in bf16
+ *   codes    = rint(127 p / A), ties to even;  scales = A r / 127 in fp32
+ *   A        = max |p| over the scale's columns
+ * The code c stands for c * scale. group 0: one scale per row, scales [T];
+ * group 32, 64 or 128: one per that many columns, scales [T, H / group].
+ * Codes are exact: bit for bit those of float64 arithmetic on the fp32 z, as
+ * rint((z * gain) * 127 / A); no rounding error of a sum enters them. All zero
+ * columns give codes 0 and scale 0. A NaN or infinity in z makes the row's
+ * scales and norm_out NaN and its codes 0 (in gain: those of its groups).
+ * x_in, y, z_out: [T,H] of dtype QMOE_F32 or QMOE_BF16; gain fp32 [H];
+ * norm_out bf16 [T,H]; codes int8 [T,H]. y, gain, z_out, norm_out may be NULL,
+ * and codes with scales; codes or norm_out must be there. z_out may alias x_in
+ * or y; no other outputs may alias inputs.
+ * Limits: H a multiple of 16 (and of group) up to 16,384, T >= 1. Alignment 16
+ * bytes, scales 4. Errors: INVALID_ARG, UNSUPPORTED (H, group). */
+qmoe_status qmoe_rmsnorm_residual_q8(const void *x_in, const void *y, int dtype, const float *gain, float eps,
+                                     int T, int H, int group, void *z_out, void *norm_out, int8_t *codes,
+                                     float *scales, qmoe_stream_t stream);
+
+/* The same quantiser without residual and norm: codes = rint(127 x / A),
+ * scales = A / 127, of T rows of H values (for example an 8-bit weight matrix,
+ * one scale per row). Values that are not finite make only their own scale
+ * NaN (with codes 0). Limits and errors as above. */
+qmoe_status qmoe_quantise_rows(const void *x, int dtype, int T, int H, int group, int8_t *codes, float *scales,
+                               qmoe_stream_t stream);
+
+/* ---------------------------------------------------------- dense product --
+ *   out[m,n] = act(s_a[m] s_w[n] sum_k a[m,k] w[n,k] + bias[n]) + residual[m,n]
+ * on the tcgen05 tensor cores, one launch for any size.
+ *   in_dtype QMOE_BF16: a [M,K], w [N,K] bf16, fp32 accumulators; a_scale and
+ *     w_scale must be NULL (s_a = s_w = 1).
+ *   in_dtype QMOE_I8: a, w int8, exact int32 accumulators, a_scale fp32 [M] and
+ *     w_scale fp32 [N]: the codes and row scales of the calls above.
+ *   out_dtype QMOE_F32 or QMOE_BF16, of out and residual (fp32 arithmetic, one
+ *     rounding); bias fp32 [N] or NULL; residual [M,N] or NULL, may be out.
+ *   act QMOE_ACT_NONE, _RELU, _SILU (v / (1 + exp(-v))), _GELU (v Phi(v)).
+ *   lda, ldw, ldr, ldo: row strides in elements, 0 = packed (K, K, N, N).
+ *     Columns past K (or N) of a row are neither read nor written.
+ * The result does not depend on timing: sums are formed in a fixed order.
+ * Limits: M, N >= 1, 1 <= K <= 65,536; rows of a and w must start on 16 bytes
+ * (lda, ldw multiples of 8 for bf16, of 16 for int8). Alignment: 16 bytes.
+ * out must not overlap a, w, the scales or bias. Errors: INVALID_ARG (null or
+ * misaligned pointers, strides below the row, scales missing or not wanted),
+ * UNSUPPORTED (K, row alignment); device status TIMEOUT if a wait inside the
+ * kernel ran out of its budget. */
+qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, int M, int N, int K, const float *a_scale,
+                        const float *w_scale, const float *bias, int act, const void *residual, void *out,
+                        int out_dtype, int64_t lda, int64_t ldw, int64_t ldr, int64_t ldo, int32_t *dev_status,
+                        qmoe_stream_t stream);
+
+/* --------------------------------------------------------------- sampling --
+ * One token per row of logits [T,V] (QMOE_F32 or QMOE_BF16, row stride ld
+ * elements, 0 = V) from a given uniform number. With m the row's largest logit:
+ *   w_i  = exp((l_i - m) / temperature[t]); 1 where l_i = m, 0 below 2^-64
+ *   rank: logit descending, ties to the lower index
+ *   kept = the first top_k[t] ranks with w_i >= min_p[t], cut to the shortest
+ *          prefix of ranks whose sum of w reaches top_p[t] times their sum
+ *   token[t] = the lowest kept index whose running sum of kept w, in index
+ *          order, exceeds u[t] times the kept sum;  prob[t] = w / kept sum
+ * Sums that decide are float64 in a fixed order: the same inputs give the same
+ * token. Masked tokens are -inf (NaN counts as -inf); a row without any
+ * candidate gives token -1 and prob 0. temperature 0 takes the largest logit
+ * (the lowest index of equals) with prob 1.
+ * temperature, top_p, min_p, u fp32 [T]; top_k int32 [T]; token int32 [T];
+ * prob fp32 [T] or NULL. A NULL temperature is 1; a NULL filter is off, and so
+ * are top_k <= 0 or >= V, top_p >= 1 and min_p <= 0. top_p <= 0 keeps one rank.
+ * Limits: T >= 1, 1 <= V <= 393,216. Alignment: logits 16 bytes (rows may start
+ * anywhere), the others 4. Errors: INVALID_ARG, UNSUPPORTED (V). A row whose
+ * temperature is negative, NaN or infinite, top_p NaN, min_p NaN or above 1, or
+ * u outside [0, 1) gets token -1, prob 0 and sets the device status, which
+ * qmoe_read_status reports as INVALID_ARG; the other rows are sampled. */
+qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, int64_t ld, const float *temperature,
+                        const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                        int32_t *token, float *prob, int32_t *dev_status, qmoe_stream_t stream);
 
 /* ------------------------------------------------------------------- misc -- */
 /* Synchronous: copies *dev_status to the host and maps it to a status. */

@@ -15,7 +15,8 @@ LIB_PATH = os.path.join(_HERE, "libqmoe.so")
 
 OK = 0
 Q2, Q4 = 2, 4
-F32, BF16 = 0, 1
+F32, BF16, I8 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
 GATE_UP, DOWN = 0, 1
 STACK_TIMING = 1
 STACK_LAYERWISE = 2
@@ -73,6 +74,11 @@ _SIGS = {
     "qmoe_stack_layer_times": (_I, [_VP, _VP, _VP]),
     "qmoe_stack_decode_host": (_I, [_VP, _VP, _VP, _VP]),
     "qmoe_ngram_gather": (_I, [_VP, _I, ctypes.c_uint64, _VP, _VP, ctypes.c_int64, _I, _VP, _VP, _VP]),
+    "qmoe_rmsnorm_residual_q8": (_I, [_VP, _VP, _I, _VP, _F, _I, _I, _I, _VP, _VP, _VP, _VP, _VP]),
+    "qmoe_quantise_rows": (_I, [_VP, _I, _I, _I, _I, _VP, _VP, _VP]),
+    "qmoe_linear": (_I, [_VP, _I, _VP, _I, _I, _I, _VP, _VP, _VP, _I, _VP, _VP, _I, ctypes.c_int64, ctypes.c_int64,
+                         ctypes.c_int64, ctypes.c_int64, _VP, _VP]),
+    "qmoe_sample": (_I, [_VP, _I, _I, _I, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
     "qmoe_read_status": (_I, [_VP]),
     "qmoe_status_string": (ctypes.c_char_p, [_I]),
     "qmoe_launch_count": (ctypes.c_uint64, []),
@@ -197,6 +203,74 @@ def qmoe_ngram_gather(ngrams, T, seed, codes, scales, R, D, out, rows=None, stre
     ``out`` fp32 [T, 16, D]; ``rows`` int32 [T, 16] or None."""
     _check("qmoe_ngram_gather", lib().qmoe_ngram_gather(_p(ngrams), T, seed & ((1 << 64) - 1), _p(codes), _p(scales),
                                                         R, D, _p(out), _p(rows), _s(stream)))
+
+
+_DTYPES = {F32: "float32", BF16: "bfloat16", I8: "int8"}
+
+
+def _fits(fn: str, *wants) -> None:
+    """(tensor or None, type, rows, columns, row stride) each: on the current device, of the type, rows dense,
+    and large enough for what the call reads or writes. A plain address (int) is the caller's word."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t, dtype, rows, cols, ld in wants:
+        if t is None or isinstance(t, int):
+            continue
+        if t.dtype != getattr(torch, dtype):
+            raise QmoeError(fn + f" (a {t.dtype} tensor in the place of a {dtype} one)", 1)
+        if t.get_device() != dev:
+            raise QmoeError(fn + " (a tensor on another device than the current one)", 1)
+        if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise QmoeError(fn + " (a tensor whose rows are not contiguous)", 1)
+        if t.dim() > 1 and ld and t.shape[-2] > 1 and t.stride(-2) != ld:
+            raise QmoeError(fn + " (a tensor whose row stride is not the one given)", 1)
+        if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < (rows - 1) * (ld or cols) + cols:
+            raise QmoeError(fn + " (a tensor smaller than the call's sizes)", 1)
+
+
+def qmoe_rmsnorm_residual_q8(x_in, y, dtype, gain, eps, T, H, group, z_out, norm_out, codes, scales, stream=None) -> None:
+    """``x_in``, ``y``, ``z_out`` fp32 or bf16 [T, H] (``dtype``); ``gain`` fp32 [H]; ``norm_out`` bf16 [T, H];
+    ``codes`` int8 [T, H]; ``scales`` fp32 [T] (``group`` 0) or [T, H / group]. Any of y, gain, z_out, norm_out
+    and (codes, scales) may be None."""
+    dt = _DTYPES.get(dtype, "float32")
+    _fits("qmoe_rmsnorm_residual_q8", (x_in, dt, T, H, H), (y, dt, T, H, H), (gain, "float32", 1, H, 0),
+          (z_out, dt, T, H, H), (norm_out, "bfloat16", T, H, H), (codes, "int8", T, H, H),
+          (scales, "float32", 1, T * (H // group if group > 0 else 1), 0))
+    _check("qmoe_rmsnorm_residual_q8", lib().qmoe_rmsnorm_residual_q8(
+        _p(x_in), _p(y), dtype, _p(gain), float(eps), T, H, group, _p(z_out), _p(norm_out), _p(codes), _p(scales),
+        _s(stream)))
+
+
+def qmoe_quantise_rows(x, dtype, T, H, group, codes, scales, stream=None) -> None:
+    """``x`` fp32 or bf16 [T, H] -> ``codes`` int8 [T, H] and ``scales`` fp32 [T] or [T, H / group]."""
+    _fits("qmoe_quantise_rows", (x, _DTYPES.get(dtype, "float32"), T, H, H), (codes, "int8", T, H, H),
+          (scales, "float32", 1, T * (H // group if group > 0 else 1), 0))
+    _check("qmoe_quantise_rows", lib().qmoe_quantise_rows(_p(x), dtype, T, H, group, _p(codes), _p(scales), _s(stream)))
+
+
+def qmoe_linear(a, in_dtype, w, M, N, K, a_scale, w_scale, bias, act, residual, out, out_dtype, dev_status, lda=0,
+                ldw=0, ldr=0, ldo=0, stream=None) -> None:
+    """out = act(a w^T scaled + bias) + residual. ``a`` [M, K] and ``w`` [N, K] bf16 (``in_dtype`` BF16) or int8
+    with ``a_scale`` fp32 [M] and ``w_scale`` fp32 [N] (I8); ``bias`` fp32 [N] or None; ``residual`` and ``out``
+    [M, N] of ``out_dtype``; strides in elements, 0 = packed."""
+    dt, odt = _DTYPES.get(in_dtype, "bfloat16"), _DTYPES.get(out_dtype, "float32")
+    _fits("qmoe_linear", (a, dt, M, K, lda or K), (w, dt, N, K, ldw or K), (a_scale, "float32", 1, M, 0),
+          (w_scale, "float32", 1, N, 0), (bias, "float32", 1, N, 0), (residual, odt, M, N, ldr or N),
+          (out, odt, M, N, ldo or N))
+    _check("qmoe_linear", lib().qmoe_linear(
+        _p(a), in_dtype, _p(w), M, N, K, _p(a_scale), _p(w_scale), _p(bias), act, _p(residual), _p(out), out_dtype,
+        lda, ldw, ldr, ldo, _p(dev_status), _s(stream)))
+
+
+def qmoe_sample(logits, dtype, T, V, temperature, top_k, top_p, min_p, u, token, prob, dev_status, ld=0,
+                stream=None) -> None:
+    """``logits`` fp32 or bf16 [T, V] (row stride ``ld`` elements, 0 = V); ``temperature``, ``top_p``, ``min_p``
+    fp32 [T] or None, ``top_k`` int32 [T] or None, ``u`` fp32 [T]; ``token`` int32 [T], ``prob`` fp32 [T] or None."""
+    _fits("qmoe_sample", (logits, _DTYPES.get(dtype, "float32"), T, V, ld or V), (temperature, "float32", 1, T, 0),
+          (top_k, "int32", 1, T, 0), (top_p, "float32", 1, T, 0), (min_p, "float32", 1, T, 0), (u, "float32", 1, T, 0),
+          (token, "int32", 1, T, 0), (prob, "float32", 1, T, 0))
+    _check("qmoe_sample", lib().qmoe_sample(_p(logits), dtype, T, V, ld, _p(temperature), _p(top_k), _p(top_p),
+                                            _p(min_p), _p(u), _p(token), _p(prob), _p(dev_status), _s(stream)))
 
 
 PREFILL_ATOMIC_COMBINE = 1

@@ -1,7 +1,7 @@
 // Host-side helpers of libqmoe: status mapping, device queries, launch counter.
 #include <atomic>
 
-#include "common.cuh"
+#include "dense.cuh"
 
 namespace qmoe {
 
@@ -52,6 +52,7 @@ extern "C" qmoe_status qmoe_read_status(const int32_t *dev_status) {
     case qmoe::DEV_OK: return QMOE_OK;
     case qmoe::DEV_TIMEOUT: return QMOE_ERR_TIMEOUT;
     case qmoe::DEV_RANGE: return QMOE_ERR_RANGE;
+    case qmoe::DEV_BAD_PARAM: return QMOE_ERR_INVALID_ARG;
     default: return QMOE_ERR_DEVICE_STATUS;
   }
 }

@@ -1,0 +1,95 @@
+"""Host-side refusals of the dense operators (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import quantised_expert_decode_b200 as q
+from quantised_expert_decode_b200 import _lib as L
+
+FAKE = 1 << 20   # aligned non-null address; never dereferenced by the host checks below
+
+
+def test_norm_argument_checks():
+    lib = q.lib()
+
+    def call(x=FAKE, y=FAKE, dt=q.F32, gain=FAKE, eps=1e-6, T=1, H=2048, group=0, z=FAKE, norm=None, codes=FAKE, scales=FAKE):
+        return lib.qmoe_rmsnorm_residual_q8(x, y, dt, gain, ctypes.c_float(eps), T, H, group, z, norm, codes, scales, None)
+
+    assert call(x=None) == 1 and call(T=0) == 1 and call(H=0) == 1 and call(dt=q.I8) == 1
+    assert call(codes=None) == 1 and call(scales=None) == 1                     # codes and scales go together
+    assert call(codes=None, scales=None) == 1                                   # nothing to write
+    for name in ("x", "y", "gain", "z", "norm", "codes"):
+        assert call(**{name: FAKE + 8}) == 1, name
+    assert call(scales=FAKE + 2) == 1
+    assert call(eps=-1.0) == 1 and call(eps=float("nan")) == 1
+    assert call(H=2040) == 3 and call(H=16400) == 3
+    assert call(group=16) == 3 and call(group=-32) == 3 and call(group=256) == 3 and call(group=128, H=2048 + 64) == 3
+
+
+def test_quantise_argument_checks():
+    lib = q.lib()
+
+    def call(x=FAKE, dt=q.BF16, T=1, H=64, group=0, codes=FAKE, scales=FAKE):
+        return lib.qmoe_quantise_rows(x, dt, T, H, group, codes, scales, None)
+
+    assert call(x=None) == 1 and call(codes=None) == 1 and call(scales=None) == 1 and call(T=0) == 1 and call(dt=5) == 1
+    assert call(x=FAKE + 4) == 1 and call(codes=FAKE + 4) == 1 and call(scales=FAKE + 1) == 1
+    assert call(H=24) == 3 and call(group=96) == 3 and call(H=32768) == 3
+
+
+def test_linear_argument_checks():
+    lib = q.lib()
+
+    def call(a=FAKE, dt=q.BF16, w=FAKE, M=4, N=64, K=64, sa=None, sw=None, bias=None, act=0, res=None, out=FAKE,
+             odt=q.F32, lda=0, ldw=0, ldr=0, ldo=0, st=FAKE):
+        return lib.qmoe_linear(a, dt, w, M, N, K, sa, sw, bias, act, res, out, odt, lda, ldw, ldr, ldo, st, None)
+
+    assert call(a=None) == 1 and call(w=None) == 1 and call(out=None) == 1 and call(st=None) == 1
+    assert call(M=0) == 1 and call(N=0) == 1 and call(K=0) == 1 and call(M=-3) == 1
+    assert call(dt=q.F32) == 1 and call(odt=q.I8) == 1 and call(act=4) == 1 and call(act=-1) == 1
+    assert call(sa=FAKE) == 1 and call(dt=q.I8) == 1 and call(dt=q.I8, sa=FAKE) == 1       # scales: 8-bit only, both
+    assert call(lda=63) == 1 and call(ldw=8) == 1 and call(ldo=63) == 1 and call(res=FAKE, ldr=60) == 1
+    assert call(lda=-64) == 1
+    for name in ("a", "w", "out", "bias", "res"):
+        assert call(**{name: FAKE + 4}) == 1, name
+    assert call(st=FAKE + 2) == 1
+    assert call(K=60) == 3 and call(K=60, lda=64) == 3 and call(K=60, lda=64, ldw=61) == 3   # rows off 16 bytes
+    assert call(K=72, dt=q.I8, sa=FAKE, sw=FAKE) == 3
+    assert call(K=65536 + 64) == 3 and call(lda=1 << 40) == 3
+
+
+def test_sample_argument_checks():
+    lib = q.lib()
+
+    def call(l=FAKE, dt=q.F32, T=2, V=100, ld=0, temp=None, k=None, p=None, mp=None, u=FAKE, tok=FAKE, prob=None, st=FAKE):
+        return lib.qmoe_sample(l, dt, T, V, ld, temp, k, p, mp, u, tok, prob, st, None)
+
+    assert call(l=None) == 1 and call(u=None) == 1 and call(tok=None) == 1 and call(st=None) == 1
+    assert call(T=0) == 1 and call(V=0) == 1 and call(ld=99) == 1 and call(ld=-1) == 1 and call(dt=q.I8) == 1
+    assert call(l=FAKE + 8) == 1
+    for name in ("temp", "k", "p", "mp", "u", "tok", "prob", "st"):
+        assert call(**{name: FAKE + 2}) == 1, name
+    assert call(V=393217) == 3
+
+
+class _OnAnotherDevice:
+    """Just enough of a tensor to be looked at."""
+
+    import torch
+    dtype = torch.float32
+
+    def get_device(self):
+        return 1
+
+
+def test_binding_refuses_tensors_that_do_not_fit(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # CPU tensors report device -1
+    x = torch.zeros(4, 64)
+    f = "float32"
+    L._fits("f", (x, f, 4, 64, 64), (x, f, 2, 64, 64), (None, f, 9, 9, 9), (123, f, 9, 9, 9))
+    L._fits("f", (x[:, :50], f, 4, 50, 64), (x[1:], f, 3, 64, 64))
+    for bad in ((x, f, 5, 64, 64), (x[1:], f, 4, 64, 64), (x.t(), f, 4, 64, 64), (x[:, :50], f, 4, 50, 50),
+                (x, "bfloat16", 4, 64, 64), (x.double(), f, 4, 64, 64), (_OnAnotherDevice(), f, 1, 1, 0)):
+        with pytest.raises(q.QmoeError):
+            L._fits("f", bad)
