@@ -60,8 +60,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 
 // Every thread of every CTA of the cluster; orders their shared-memory accesses.
+// Not the .aligned form: the callers' warps may have diverged.
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // This CTA's shared object as it lies in CTA `rank` of the cluster (generic address).

@@ -9,15 +9,34 @@
 // The pages sample nothing; the rule is self-defined.
 //
 // Every filter keeps a prefix of the ranks, so the kept set is described by its
-// last element: a border (value, index). The row is read from HBM once, into
-// the shared memory of a cluster of CTAs (a contiguous slice each), and the
-// border is found there without sorting: a histogram over the value range
-// locates the bin that the border falls into, exact sums over the row confirm
-// it, and the bin's few elements are ranked one by one; a bin that is still
-// too large is cut again. Sums that decide are float64, formed in a fixed
-// order, so the same inputs give the same token on every run.
+// last element: a border (value, index). It is found without sorting the row.
+//
+// Where the row lives: few rows are each spread over a cluster of CTAs, every
+// CTA with a contiguous slice of the row in shared memory (`RES`; one read from
+// HBM). Many rows are taken by one CTA each, which reads its row three times,
+// twice out of L2: no cluster barriers, and enough rows in flight.
+//
+// How the border is found:
+// quick - one pass builds a histogram over 2048 value bins (counts for top-k,
+//   masses for top-p) beside the row's sum of fp32 weights with its error bound;
+//   the few bins that the border can lie in are gathered, sorted, and summed in
+//   rank order with float64 weights (a table and a polynomial, relative error
+//   below 4e-12); what lies above those bins is summed in the same precision,
+//   for each stretch of 256 logits apart, packed so that whole warps form the
+//   weights of kept logits only; the stretch that the token falls into is then
+//   gone through element by element. Every decision is checked to be further
+//   from its border than the error bound of the sums; where the fp32 sum is too
+//   coarse the row's sum is formed again in float64, and where that leaves it
+//   open too, or the bins do not separate the row, the row is done the exact way.
+// exact - float64 exp, sums over the row confirm every bin, and a bin that holds
+//   more than a list is cut again, down to equal values ordered by index.
+//
+// Either way sums that decide are float64 in a fixed order: the same inputs give
+// the same token on every run. Within a warp's part, elements go in rounds of
+// 128, four neighbours per lane.
 #include <cuda_bf16.h>
 #include <math_constants.h>
+#include <stddef.h>
 
 #include "dense.cuh"
 
@@ -26,11 +45,15 @@ namespace {
 
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
-constexpr int SP_BINS = 1024;
+constexpr int SP_BINS = 1024;                 // exact way
+constexpr int SQ_BINS = 2048;                 // quick way: 11 bits of bin, 12 bits of place within it
+constexpr int SQ_ROUND = 256;                 // logits of a warp whose sums are kept apart: two float4 per lane
+constexpr int SQ_LIST = 1024;                 // elements that the quick way gathers and sorts
+constexpr double SP_EPS = 1e-11;              // bound of the quick sums' error, relative to the row's sum
 constexpr int SP_LIST = SP_THREADS;           // elements ranked one by one (one per thread)
 constexpr int SP_MAX_CLUSTER = 8;
-constexpr int SP_MAX_SLICE = 49152;           // 192 KB of fp32 logits per CTA
-constexpr int SP_MAX_V = SP_MAX_CLUSTER * SP_MAX_SLICE;
+constexpr int SP_MAX_SLICE = 32768;           // 128 KB of fp32 logits per CTA
+constexpr int SP_MAX_V = 393216;
 constexpr double SP_W_MIN = 5.421010862427522e-20;   // 2^-64
 constexpr int SP_FIX = 44;                    // histogram masses in units of 2^-44
 constexpr float SP_LOWEST = -3.402823466e38f;
@@ -45,31 +68,87 @@ struct SpArgs {
   int32_t *status;
   long long ld;
   int T, V, slice, nc;       // nc: CTAs per row
+  int seg;                   // a warp's part of the slice, a multiple of 128
 };
 
-// What one CTA contributes to a sum over the cluster.
+// What one CTA contributes to a step of the exact way.
 struct SpPart {
   double above, in;          // weight above the bin, in the bin
   float min_above, max_in, min_in, max_below;
   int n_in, pad;
 };
 
+// What a CTA pushes into every CTA of its cluster.
+struct SpPush {
+  double a, b;
+  float c;
+  int bad;
+};
+
 struct SpShared {
   SpPart part[2];
+  SpPush push[7][SP_MAX_CLUSTER];
   double warp_d[2][SP_WARPS];
+  double exp2_tab[32];       // 2^(i / 32)
   float warp_f[4][SP_WARPS];
   int warp_i[SP_WARPS];
-  unsigned long long mass[SP_BINS];
+  union {
+    unsigned long long mass[SP_BINS];         // exact way
+    alignas(16) unsigned int bins[SQ_BINS];   // quick way: histogram, read four at a time
+    double w[SQ_LIST];                        // quick way: weights of the sorted list
+  };
+  union {
+    struct {                                  // exact way
+      float list_v[SP_LIST];
+      int list_i[SP_LIST];
+      float sort_v[SP_LIST];
+      int sort_i[SP_LIST];
+    };
+    unsigned long long keys[SQ_LIST];         // quick way: sq_key of gathered elements
+  };
+  double rounds[SP_WARPS][SP_MAX_V / SP_WARPS / SQ_ROUND];
   unsigned int list_n;
-  int found;
-  float list_v[SP_LIST];
-  int list_i[SP_LIST];
-  float sort_v[SP_LIST];
-  int sort_i[SP_LIST];
+  int found, last;
   float border_v;
-  int border_i;
-  float live;
+  int border_i, bad;
+  double open_sum;
+  float live, q_lo, q_hi;
 };
+
+static_assert(offsetof(SpShared, bins) % 16 == 0 && alignof(SpShared) == 16, "bins are read as uint4");
+
+// A CTA's slice of a row: in shared memory (RES) or in global memory. NaN
+// stays: it passes no comparison.
+template <bool BF16, bool RES>
+struct SpSrc {
+  const void *row;
+  const float *vals;
+  int n;
+  bool vec;   // rows of memory start where four logits can be read at once
+  __device__ __forceinline__ float at(int i) const {
+    if (RES) return vals[i];
+    return BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[i]) : static_cast<const float *>(row)[i];
+  }
+  // Four neighbours from i (a multiple of 4); -inf from `end` on.
+  __device__ __forceinline__ float4 four(int i, int end) const {
+    if (RES) {
+      if (i >= end) return make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+      return *reinterpret_cast<const float4 *>(vals + i);   // -inf behind the slice
+    }
+    if (vec && i + 4 <= end) {
+      if (!BF16) return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + i));
+      const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(row) + i));
+      return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                         __uint_as_float(q.y & 0xffff0000u));
+    }
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = i + j < end ? at(i + j) : -CUDART_INF_F;
+    return make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+
+__host__ __device__ constexpr size_t sp_head_bytes() { return (sizeof(SpShared) + 15) & ~(size_t)15; }
 
 struct SpRow {
   float max;
@@ -151,8 +230,8 @@ __device__ double sp_cluster_sum(double v, SpShared *sh, const SpArgs &a, int &p
 // The border of the shortest prefix of ranks whose sum of weights (COUNT: of
 // ones) reaches `target`, among the kept elements. Leaves r as it is when the
 // kept elements do not reach it.
-template <bool COUNT>
-__device__ void sp_select(const float *vals, int n, int base, SpRow &r, double target, SpShared *sh, const SpArgs &a,
+template <bool COUNT, typename Src>
+__device__ void sp_select(const Src &src, int n, int base, SpRow &r, double target, SpShared *sh, const SpArgs &a,
                           int rank, int &par) {
   const int tid = threadIdx.x;
   float vhi = r.max, vlo = fmaxf(r.live, r.bv);
@@ -168,7 +247,7 @@ __device__ void sp_select(const float *vals, int n, int base, SpRow &r, double t
     for (int i = tid; i < SP_BINS; i += SP_THREADS) sh->mass[i] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += SP_THREADS) {
-      const float l = vals[i];
+      const float l = src.at(i);
       if (l <= vhi && l >= vlo && sp_kept(l, base + i, r)) {
         const unsigned long long q =
             COUNT ? 1ull : (unsigned long long)__double2ll_rn(sp_weight(l, r) * (double)(1ull << SP_FIX));
@@ -212,7 +291,7 @@ __device__ void sp_select(const float *vals, int n, int base, SpRow &r, double t
     float min_above = CUDART_INF_F, max_in = -CUDART_INF_F, min_in = CUDART_INF_F, max_below = -CUDART_INF_F;
     int n_in = 0;
     for (int i = tid; i < n; i += SP_THREADS) {
-      const float l = vals[i];
+      const float l = src.at(i);
       if (l <= vhi && l >= vlo && sp_kept(l, base + i, r)) {
         const int b = bin_of(l);
         const double w = COUNT ? 1.0 : sp_weight(l, r);
@@ -297,7 +376,7 @@ __device__ void sp_select(const float *vals, int n, int base, SpRow &r, double t
       // rank the bin's elements: gathered in CTA 0, sorted by counting, summed in rank order
       SpShared *s0 = dense::peer(sh, 0);
       for (int i = tid; i < n; i += SP_THREADS) {
-        const float l = vals[i];
+        const float l = src.at(i);
         if (l <= vhi && l >= vlo && sp_kept(l, base + i, r)) {
           const unsigned at = atomicAdd(&s0->list_n, 1u);
           s0->list_v[at] = l;
@@ -360,7 +439,7 @@ __device__ void sp_select(const float *vals, int n, int base, SpRow &r, double t
     const int seg = (a.slice + SP_WARPS - 1) / SP_WARPS, wid = tid >> 5, lane = tid & 31;
     const int s0i = wid * seg, s1i = min(n, s0i + seg);
     int cnt = 0;
-    for (int i = s0i + lane; i < s1i; i += 32) cnt += vals[i] == vhi && sp_kept(vals[i], base + i, r);
+    for (int i = s0i + lane; i < s1i; i += 32) cnt += src.at(i) == vhi && sp_kept(src.at(i), base + i, r);
     cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) sh->warp_i[wid] = cnt;
     __syncthreads();
@@ -383,7 +462,7 @@ __device__ void sp_select(const float *vals, int n, int base, SpRow &r, double t
       if (b2 < want && b2 + sh->warp_i[wid] >= want) {
         for (int i0 = s0i; i0 < s1i; i0 += 32) {
           const int i = i0 + lane;
-          const bool eq = i < s1i && vals[i] == vhi && sp_kept(vals[i], base + i, r);
+          const bool eq = i < s1i && src.at(i) == vhi && sp_kept(src.at(i), base + i, r);
           const unsigned mask = __ballot_sync(0xffffffffu, eq);
           const int c = __popc(mask);
           if (b2 + c >= want) {
@@ -404,13 +483,679 @@ __device__ void sp_select(const float *vals, int n, int base, SpRow &r, double t
   set_status(a.status, DEV_TIMEOUT);
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(SP_THREADS) sample_kernel(SpArgs a) {
+// ------------------------------------------------------------------ quick way --
+struct SqRow {
+  float m;          // largest logit, finite
+  double c, mc;     // log2(e) / temperature, and its product with m
+  float cut;        // logits below have no weight
+  float low;        // smallest logit with one
+  float scale;      // bins: place = (m - l) * scale, in [0, 2^23) from `low` up
+};
+
+// 2^z for z = (l - m) log2(e) / temperature: z to the nearest 1/32, a table for
+// that and the Taylor polynomial of degree 4 for the rest (|r| <= 1/64, so the
+// next term is below (ln2 / 64)^5 / 120 = 1.3e-12).
+__device__ __forceinline__ double sq_weight(float l, const SqRow &r, const double *tab) {
+  const double z = fma((double)fmaxf(l, r.cut), r.c, -r.mc);
+  const double magic = 211106232532992.0;   // 1.5 * 2^47: the sum's low word is z in units of 1/32
+  const double t = z + magic;
+  const int k = __double2loint(t);
+  const double f = z - (t - magic);
+  double p = fma(f, 0.009618129107628477, 0.05550410866482158);
+  p = fma(f, p, 0.2402265069591007);
+  p = fma(f, p, 0.6931471805599453);
+  const double T = tab[k & 31];
+  const double S = __hiloint2double(__double2hiint(T) + (k >> 5) * 0x100000, __double2loint(T));
+  const double w = fma(S, f * p, S);
+  return l >= r.cut ? w : 0.0;
+}
+
+// The same in fp32 and y = -z: the hardware exponential (2^-22 relative) of a
+// product with three roundings (1.3e-7 of y).
+__device__ __forceinline__ float sq_fast(float l, float c32, const SqRow &r, float &y) {
+  y = fminf(__fmul_rn(__fsub_rn(r.m, l), c32), 64.0f);
+  float w;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(-y));
+  return w;
+}
+
+// Place of a logit >= low among the bins: 11 bits of bin, 12 bits inside it.
+// Grows monotonically as the logit falls (two roundings of monotone operations).
+// As a float it is 2^23 + place, exactly: the low 23 bits hold the place.
+__device__ __forceinline__ float sq_place(float l, const SqRow &r) {
+  return __fmaf_rn(__fsub_rn(r.m, l), r.scale, 8388608.0f);
+}
+__device__ __forceinline__ unsigned sq_bin(float place) { return (__float_as_uint(place) & 0x7fffffu) >> 12; }
+// The place where bin b begins (b up to 2048).
+__device__ __forceinline__ float sq_bin_at(unsigned b) { return 8388608.0f + 4096.0f * (float)b; }
+
+template <typename T>
+__device__ __forceinline__ void push_all(T *at, const T &v, int nc) {
+  for (int c = 0; c < nc; ++c) *dense::peer(at, c) = v;
+}
+
+// Ascending keys are ascending ranks: logit descending, then index.
+__device__ __forceinline__ unsigned long long sq_key(float l, int i) {
+  return ((unsigned long long)~float_key(l) << 32) | (unsigned)i;
+}
+__device__ __forceinline__ float sq_key_logit(unsigned long long k) { return key_float(~(unsigned)(k >> 32)); }
+
+// Sorts the n keys, ascending (all threads of the CTA; a bitonic network, one
+// pair per thread).
+__device__ void sq_sort(SpShared *sh, int n) {
+  const int tid = threadIdx.x;
+  int size = 2;
+  while (size < n) size *= 2;
+  for (int i = n + tid; i < size; i += SP_THREADS) sh->keys[i] = ~0ull;
+  __syncthreads();
+  for (int k = 2; k <= size; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      if (tid < size / 2) {
+        const int a = 2 * tid - (tid & (j - 1)), b = a + j;
+        const unsigned long long x = sh->keys[a], y = sh->keys[b];
+        if ((x > y) == ((a & k) == 0)) {
+          sh->keys[a] = y;
+          sh->keys[b] = x;
+        }
+      }
+      if (j > 32) __syncthreads();
+      else __syncwarp();   // up to there a warp's pairs stay within its own 64 keys
+      if (j == 1) __syncthreads();
+    }
+}
+
+// The gathered keys in rank order, and their weights.
+__device__ void sq_rank(SpShared *sh, int n, const SqRow &r) {
+  sq_sort(sh, n);
+  for (int i = threadIdx.x; i < n; i += SP_THREADS) sh->w[i] = sq_weight(sq_key_logit(sh->keys[i]), r, sh->exp2_tab);
+  __syncthreads();
+}
+
+// The element of a list of n weights where the running sum (from A) first
+// reaches `target`: its place, or -1; `sure` is false where a running sum on
+// either side of it is within eps of the target. One warp.
+template <typename W>
+__device__ int sq_cross(W weight, int n, double A, double target, double eps, bool &sure) {
+  const int lane = threadIdx.x & 31;
+  double run = A;
+  for (int c = 0; c < n; c += 32) {
+    const int j = c + lane;
+    double x = j < n ? weight(j) : 0.0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const double after = run + x;
+    const unsigned ok = __ballot_sync(0xffffffffu, j < n && after >= target);
+    if (ok) {
+      const int h = __ffs(ok) - 1;
+      const double up = __shfl_sync(0xffffffffu, after, h), prev = __shfl_sync(0xffffffffu, after, h > 0 ? h - 1 : 0);
+      const double below = h > 0 ? prev : run;
+      sure = up - target > eps && target - below > eps;
+      return c + h;
+    }
+    run += __shfl_sync(0xffffffffu, x, 31);
+  }
+  sure = false;
+  return -1;
+}
+
+// Running sums over the warps of a CTA, in warp order, of a value per warp that
+// lanes 0 bring: the sum before warp w in lane w, the whole sum in every lane.
+// Between two uses of one buf lies a CTA barrier.
+__device__ __forceinline__ void sq_cta_scan(double v, double *buf, double &before, double &whole) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const double own = lane < SP_WARPS ? buf[lane] : 0.0;
+  double x = own;
+#pragma unroll
+  for (int o = 1; o < SP_WARPS; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  before = x - own;
+  whole = __shfl_sync(0xffffffffu, x, SP_WARPS - 1);
+}
+
+__device__ __forceinline__ double sq_cta_sum(double v, double *buf) {
+  double before, whole;
+  sq_cta_scan(v, buf, before, whole);
+  return whole;
+}
+
+// f(i, l): a warp's part of a row in rounds of 256, i the place of the round in
+// the part. Lane's elements: l[0..3] at i + 4 lane, l[4..7] at i + 128 + 4 lane;
+// -inf behind the part. The next round's loads are under way meanwhile.
+template <typename Src, typename F>
+__device__ __forceinline__ void sq_each(const Src &src, int s0, int own, F f) {
+  const int at = s0 + 4 * (threadIdx.x & 31), end = s0 + own;
+  float4 a = src.four(at, end), b = src.four(at + 128, end);
+#pragma unroll 1
+  for (int i = 0; i < own; i += SQ_ROUND) {
+    const float l[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    a = src.four(at + i + SQ_ROUND, end);
+    b = src.four(at + i + SQ_ROUND + 128, end);
+    f(i, l);
+  }
+}
+
+// The lane's elements (as sq_each gives them) whose bits are set, to a list.
+template <typename Src>
+__device__ __forceinline__ void sq_gather(const Src &src, SpShared *list, int i, unsigned bits, int base) {
+  for (; bits; bits &= bits - 1) {
+    const int j = __ffs(bits) - 1, e = i + 4 * (threadIdx.x & 31) + (j & 3) + 32 * (j & 4);
+    const unsigned k = atomicAdd(&list->list_n, 1u);
+    if (k < SQ_LIST) list->keys[k] = sq_key(src.at(e), base + e);
+  }
+}
+
+// Top-k: everything down to rank k's bin goes to CTA 0, which finishes the row.
+template <typename Src>
+__device__ bool sq_finish_k(const Src &src, int s0, int own, int base, float hi, float end, int top_k, float top_p, float u,
+                            const SqRow &r, SpShared *sh, const SpArgs &a, int t, int rank) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  SpShared *first = dense::peer(sh, 0);
+  sq_each(src, s0, own, [&](int i, const float(&l)[8]) {
+    unsigned in = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) in |= l[j] >= hi && sq_place(l[j], r) < end ? 1u << j : 0u;
+    sq_gather(src, first, s0 + i, in, base);
+  });
+  dense::cluster_sync();
+  if (rank == 0) {
+    int kept = (int)sh->list_n;
+    bool good = kept <= SQ_LIST;
+    if (good) {
+      sq_rank(sh, kept, r);
+      kept = min(kept, top_k);
+      if (tid < 32) {
+        double tot = 0.0;
+        for (int j = lane; j < kept; j += 32) tot += sh->w[j];
+        tot = warp_sum_d(tot);
+        if (top_p < 1.0f) {
+          const double need = (double)fmaxf(top_p, 0.0f) * tot;
+          int h = 0;
+          if (need > 0.0) {
+            bool sure = true;
+            h = sq_cross([&](int j) { return sh->w[j]; }, kept, 0.0, need, SP_EPS * tot, sure);
+            good = sure && h >= 0;
+          }
+          kept = h + 1;
+          tot = 0.0;
+          for (int j = lane; j < kept; j += 32) tot += sh->w[j];
+          tot = warp_sum_d(tot);
+        }
+        if (lane == 0) {
+          sh->warp_d[0][0] = tot;
+          sh->warp_i[0] = good ? kept : 0;
+        }
+      }
+      __syncthreads();
+      kept = sh->warp_i[0];
+      // by index: the kept elements as (index, rank)
+      unsigned long long mine[SQ_LIST / SP_THREADS];
+#pragma unroll
+      for (int c = 0; c < SQ_LIST / SP_THREADS; ++c) {
+        const int j = c * SP_THREADS + tid;
+        mine[c] = j < kept ? (sh->keys[j] << 32) | (unsigned)j : ~0ull;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < SQ_LIST / SP_THREADS; ++c) sh->keys[c * SP_THREADS + tid] = mine[c];
+      sq_sort(sh, kept);
+      if (tid < 32) {
+        const double tot = sh->warp_d[0][0];
+        bool sure = true;
+        const int h = sq_cross([&](int j) { return sh->w[(unsigned)sh->keys[j]]; }, kept, 0.0, (double)u * tot, SP_EPS * tot, sure);
+        good = sure && h >= 0;
+        if (good && lane == 0) {
+          a.token[t] = (int)(sh->keys[h] >> 32);
+          if (a.prob) a.prob[t] = (float)(sh->w[(unsigned)sh->keys[h]] / tot);
+        }
+      }
+    }
+    if (tid == 0) push_all(&sh->push[4][0], SpPush{0.0, 0.0, 0.0f, good ? 0 : 1}, a.nc);
+  }
+  dense::cluster_sync();
+  return sh->push[4][0].bad == 0;
+}
+
+// Samples the row by the quick way. Returns false (in every thread of the
+// cluster) where it cannot be sure. Its last step is a cluster barrier.
+template <bool BF16, bool RES>
+__device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, float m, float lmin, float temp,
+                       int top_k, float top_p, float min_p, float u, SpShared *sh, const SpArgs &a, int t, int rank) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, n = src.n;
+  SqRow r;
+  r.m = m;
+  r.c = 1.4426950408889634 / (double)temp;
+  r.mc = (double)m * r.c;
+  const bool k_on = top_k > 0 && top_k < a.V, p_on = top_p < 1.0f, mp_on = min_p > 0.0f;
+  // weights below 2^-63.9 are left out (their sum stays far below SP_EPS)
+  const double cut = (double)m - 44.29 * (double)temp;
+  r.cut = cut > (double)SP_LOWEST ? __double2float_ru(cut) : SP_LOWEST;
+  const float range = __fsub_rn(m, fmaxf(lmin, r.cut));
+  r.scale = __fdiv_rn(8380000.0f, range);   // a little below 2^23 / range
+  if (!(range > 0.0f && r.scale < 1e30f && r.scale > 1e-30f && r.c < 1e30 && r.c > 1e-30)) return false;
+  // min-p: kept from `hi` up, undecided from `lo` up
+  if (mp_on && tid == 0) {
+    const double at = (double)m + (double)temp * log((double)min_p), d = 1e-10 * (double)temp + 1e-14 * fabs(at);
+    sh->q_hi = __double2float_ru(at + d);
+    sh->q_lo = __double2float_ru(at - d);
+  }
+  if (tid >= SP_THREADS - 32) sh->exp2_tab[lane] = exp2((double)lane * 0.03125);
+  if (k_on || p_on)
+    for (int i = tid; i < SQ_BINS; i += SP_THREADS) sh->bins[i] = 0;
+  __syncthreads();
+  float lo = r.cut, hi = r.cut;
+  if (mp_on) {
+    lo = fmaxf(lo, sh->q_lo);
+    hi = fminf(fmaxf(hi, sh->q_hi), m);   // the largest logit is always kept
+  }
+  const int s0 = wid * a.seg;                           // this warp's part, in index order
+  const int own = max(0, min(n, s0 + a.seg) - s0);      // elements of it
+  int bad = 0;
+
+  const float c32 = (float)r.c;
+  unsigned first = SQ_BINS, last = SQ_BINS - 1;   // the border lies in these bins
+  double S = 0.0, SY = 0.0;   // the row's sum of fp32 weights, and of weights times y
+  if (k_on || p_on) {
+    const float per_bin = (float)(r.c * 4096.0 / (double)r.scale);   // log2 of the weights' fall over a bin
+    // a mass is 32768 at its bin's top, less by the weights' fall towards the bin's end
+    const unsigned slope = (unsigned)(32768.0f * (1.0f - exp2f(-per_bin)));
+    double s = 0.0;
+    float sy = 0.0f;
+    sq_each(src, s0, own, [&](int, const float(&l)[8]) {
+      if (mp_on)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) bad |= l[j] >= lo && l[j] < hi;
+      if (k_on) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (l[j] >= hi) atomicAdd(&sh->bins[sq_bin(sq_place(l[j], r))], 1u);
+        return;
+      }
+      // the sum of fp32 weights beside the histogram, two at a time in fp32
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        float w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool in = l[j + k] >= hi;
+          float y;
+          w[k] = sq_fast(l[j + k], c32, r, y);
+          w[k] = in ? w[k] : 0.0f;
+          sy = __fmaf_rn(w[k], y, sy);
+          const unsigned at = __float_as_uint(sq_place(l[j + k], r)) & 0x7fffffu;
+          if (in) atomicAdd(&sh->bins[at >> 12], ((32768u << 12) - (at & 4095u) * slope) >> 12);
+        }
+        s += (double)(w[0] + w[1]);
+      }
+    });
+    bad = __syncthreads_or(bad);
+    if (!k_on) {
+      s = sq_cta_sum(warp_sum_d(s), sh->warp_d[0]);
+      sy = (float)sq_cta_sum((double)warp_sum(sy), sh->warp_d[1]);
+    }
+    if (tid == 0) {
+      push_all(&sh->push[0][rank], SpPush{s, (double)sy, 0.0f, bad}, a.nc);
+      sh->found = sh->last = SQ_BINS;
+      sh->list_n = 0;
+    }
+    dense::cluster_sync();
+    for (int c = 0; c < a.nc; ++c) {
+      S += sh->push[0][c].a;
+      SY += sh->push[0][c].b;
+      bad |= sh->push[0][c].bad;
+    }
+    if (bad) return false;
+    // every CTA adds its share of the bins over the cluster (PER neighbouring
+    // bins per thread), then the shares' sums go round
+    constexpr int PER = SQ_BINS / SP_THREADS;
+    static_assert(PER == 4, "one uint4 of bins per thread");
+    const int share = SP_THREADS / a.nc;   // threads with bins; nc is a power of two
+    const int b0 = PER * (rank * share + tid);
+    unsigned long long hh[PER] = {0, 0, 0, 0};
+    if (tid < share) {
+      uint4 x[SP_MAX_CLUSTER];
+#pragma unroll
+      for (int c = 0; c < (RES ? SP_MAX_CLUSTER : 1); ++c)   // all loads in flight together
+        if (c < a.nc) x[c] = reinterpret_cast<const uint4 *>(dense::peer(&sh->bins[0], c))[b0 / 4];
+#pragma unroll
+      for (int c = 0; c < (RES ? SP_MAX_CLUSTER : 1); ++c)
+        if (c < a.nc) {
+          hh[0] += x[c].x;
+          hh[1] += x[c].y;
+          hh[2] += x[c].z;
+          hh[3] += x[c].w;
+        }
+    }
+    double f[PER], run = 0.0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      f[j] = (double)hh[j];
+      if (!k_on) f[j] *= (double)exp2f(-per_bin * (float)(b0 + j));
+      run += f[j];
+    }
+    double incl = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    double before, all;
+    __syncthreads();
+    sq_cta_scan(__shfl_sync(0xffffffffu, incl, 31), sh->warp_d[1], before, all);
+    double pre = __shfl_sync(0xffffffffu, before, wid) + incl - run;
+    if (RES) {
+      if (tid == 0) push_all(&sh->push[5][rank], SpPush{all, 0.0, 0.0f, 0}, a.nc);
+      dense::cluster_sync();
+      all = 0.0;
+      for (int c = 0; c < a.nc; ++c) {
+        if (c < rank) pre += sh->push[5][c].a;
+        all += sh->push[5][c].a;
+      }
+    }
+    // top-k: the bin of rank k. top-p: the bins that the histogram's masses,
+    // good to 1.3e-4, leave open.
+    const double want = k_on ? fmin((double)top_k, all) : (double)fmaxf(top_p, 0.0f) * all;
+    const double early = k_on ? want : want * (1.0 - 3e-4), late = k_on ? want : want * (1.0 + 3e-4);
+    int at_first = SQ_BINS, at_last = SQ_BINS;
+    double upto = pre;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      upto += f[j];
+      if (hh[j] && upto >= early) at_first = min(at_first, b0 + j);
+      if (hh[j] && upto >= late) at_last = min(at_last, b0 + j);
+    }
+    at_first = __reduce_min_sync(0xffffffffu, at_first);
+    at_last = __reduce_min_sync(0xffffffffu, at_last);
+    if (lane < a.nc) {
+      if (at_first < SQ_BINS) atomicMin(&dense::peer(sh, lane)->found, at_first);
+      if (at_last < SQ_BINS) atomicMin(&dense::peer(sh, lane)->last, at_last);
+    }
+    dense::cluster_sync();
+    first = (unsigned)sh->found;
+    last = (unsigned)min(sh->last, SQ_BINS - 1);
+    if (first >= SQ_BINS) return false;
+  }
+  const float end = sq_bin_at(last + 1), open = sq_bin_at(first);   // places
+  if (k_on) return sq_finish_k(src, s0, own, base, hi, end, top_k, top_p, u, r, sh, a, t, rank);
+
+  // The sum above the open bins, for each of the warp's rounds; the open bins'
+  // elements to CTA 0. Every lane stacks what it keeps of a round.
+  float *mine = stack + wid * SQ_ROUND + lane;
+  SpShared *lists = dense::peer(sh, 0);
+  double ws = 0.0, a_fast = 0.0;   // exact weights; fp32 weights of the same
+  float a_sy = 0.0f;
+  sq_each(src, s0, own, [&](int i, const float(&l)[8]) {
+    int held = 0;   // of this lane
+    unsigned opens = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      bool in = l[j] >= hi;
+      if (p_on) {
+        const float place = sq_place(l[j], r);
+        opens |= in && place >= open && place < end ? 1u << j : 0u;
+        in = in && place < open;
+      } else {
+        bad |= l[j] >= lo && !in;
+      }
+      if (in) mine[32 * held++] = l[j];
+    }
+    if (opens) sq_gather(src, lists, s0 + i, opens, base);
+    const int most = __reduce_max_sync(0xffffffffu, held);
+    double x = 0.0;
+#pragma unroll 1
+    for (int k = 0; k < most; k += 2) {   // (behind a lane's own: stale logits, not counted)
+      double w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool in = k + j < held;
+        const float m2 = mine[32 * (k + j)];
+        w[j] = sq_weight(in ? m2 : -CUDART_INF_F, r, sh->exp2_tab);
+        float y, v = sq_fast(m2, c32, r, y);
+        v = in ? v : 0.0f;
+        a_fast += (double)v;
+        a_sy = in ? __fmaf_rn(v, y, a_sy) : a_sy;
+      }
+      x += w[0] + w[1];
+    }
+    x = most ? warp_sum_d(x) : 0.0;
+    if (lane == 0) sh->rounds[wid][i / SQ_ROUND] = x;
+    ws += x;
+  });
+  bad = __syncthreads_or(bad);
+  double warps_before, sum;
+  sq_cta_scan(ws, sh->warp_d[0], warps_before, sum);
+  if (p_on) {
+    a_fast = sq_cta_sum(warp_sum_d(a_fast), sh->warp_d[1]);
+    __syncthreads();
+    a_sy = (float)sq_cta_sum((double)warp_sum(a_sy), sh->warp_d[1]);
+  }
+  if (tid == 0) push_all(&sh->push[1][rank], SpPush{sum, a_fast, a_sy, bad}, a.nc);
+  dense::cluster_sync();
+  double total = 0.0;
+  for (int c = 0; c < a.nc; ++c) {
+    total += sh->push[1][c].a;
+    S -= sh->push[1][c].b;       // what is left is below the border's bins, or in them
+    SY -= sh->push[1][c].c;
+    bad |= sh->push[1][c].bad;
+  }
+  if (bad) return false;
+
+  float bv = hi;
+  int bi = a.V;
+  if (p_on) {
+    const double p = (double)fmaxf(top_p, 0.0f);
+    const int listed = (int)lists->list_n;
+    if (listed > SQ_LIST) return false;
+    // The row's sum: exact weights down to the open bins, fp32 weights below
+    // them. Its error: 1.4e-7 of y and 2.4e-7 of each weight below, and the
+    // roundings of two weights added in fp32 of the whole first sum.
+    double whole = total + S, err = 0.0;
+    if (rank == 0) {
+      sq_rank(sh, listed, r);
+      double open_fast = 0.0, open_sum = 0.0;
+      float open_sy = 0.0f;
+      for (int j = tid; j < listed; j += SP_THREADS) {
+        float y;
+        const float v = sq_fast(sq_key_logit(sh->keys[j]), c32, r, y);
+        open_fast += (double)v;
+        open_sum += sh->w[j];
+        open_sy += v * y;
+      }
+      open_fast = sq_cta_sum(warp_sum_d(open_fast), sh->warp_d[0]);
+      open_sum = sq_cta_sum(warp_sum_d(open_sum), sh->warp_d[1]);
+      __syncthreads();
+      open_sy = (float)sq_cta_sum((double)warp_sum(open_sy), sh->warp_d[0]);
+      S -= open_fast;
+      SY -= (double)open_sy;
+      whole = total + open_sum + S;
+      err = p * (1.4e-7 * fmax(SY, 0.0) + 2.6e-7 * fmax(S, 0.0) + 8e-8 * whole);
+    }
+    for (int round = 0; round < 2; ++round) {   // (uniform over the cluster)
+      if (rank == 0 && tid < 32) {
+        bool sure = true;
+        int h = 0;
+        if (p > 0.0) h = sq_cross([&](int j) { return sh->w[j]; }, listed, total, p * whole, err, sure);
+        const int good = sure && h >= 0;
+        double x = 0.0;   // the open bins' kept weights
+        for (int j = lane; j <= h; j += 32) x += sh->w[j];
+        x = warp_sum_d(x);
+        if (lane < a.nc) {
+          SpShared *o = dense::peer(sh, lane);
+          o->border_v = good ? sq_key_logit(sh->keys[h]) : 0.0f;
+          o->border_i = good ? (int)(unsigned)sh->keys[h] : 0;
+          o->found = h;
+          o->open_sum = x;
+          o->bad = !good;
+        }
+      }
+      dense::cluster_sync();
+      if (!sh->bad) break;
+      if (round == 1) return false;
+      // the fp32 sum leaves it open: the row's sum again, in float64
+      double s = 0.0;
+#pragma unroll 4
+      for (int i = lane; i < own; i += 32) {
+        const float l = src.at(s0 + i);
+        s += sq_weight(l >= hi ? l : -CUDART_INF_F, r, sh->exp2_tab);
+      }
+      s = sq_cta_sum(warp_sum_d(s), sh->warp_d[1]);
+      if (tid == 0) push_all(&sh->push[2][rank], SpPush{s, 0.0, 0.0f, 0}, a.nc);
+      dense::cluster_sync();
+      whole = 0.0;
+      for (int c = 0; c < a.nc; ++c) whole += sh->push[2][c].a;
+      err = SP_EPS * whole;
+    }
+    bv = sh->border_v;
+    bi = sh->border_i;
+    total += sh->open_sum;
+    // the open bins' kept weights to the rounds that they lie in (what these
+    // sums decide is checked against SP_EPS, so their order does not matter)
+    for (int j = tid; j <= sh->found; j += SP_THREADS) {
+      const int i = (int)(unsigned)lists->keys[j] - base;
+      if (i >= 0 && i < n) atomicAdd(&sh->rounds[i / a.seg][i % a.seg / SQ_ROUND], lists->w[j]);
+    }
+    __syncthreads();
+    ws = 0.0;
+    for (int i = lane; i * SQ_ROUND < own; i += 32) ws += sh->rounds[wid][i];
+    ws = warp_sum_d(ws);
+    sq_cta_scan(ws, sh->warp_d[1], warps_before, sum);
+    if (tid == 0) push_all(&sh->push[3][rank], SpPush{sum, 0.0, 0.0f, 0}, a.nc);
+    dense::cluster_sync();
+  }
+
+  // the token, by index: the CTA, the warp, the round, the lane's elements, the element
+  const SpPush *sums = p_on ? sh->push[3] : sh->push[1];
+  const double aim = (double)u * total, eps = SP_EPS * total;
+  double before = 0.0;
+  int owner = -1;
+  for (int c = 0; c < a.nc && owner < 0; ++c) {
+    const double x = sums[c].a;
+    if (before + x > aim) owner = c;
+    else before += x;
+  }
+  if (owner < 0) return false;
+  if (rank == owner) {
+    // the last warp that begins at or below the target (the first begins at `before`)
+    const unsigned starts = __ballot_sync(0xffffffffu, lane < SP_WARPS && before + warps_before <= aim);
+    if (wid == (starts ? 31 - __clz(starts) : 0)) {
+      auto scan = [&](double v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += y;
+        }
+        return v;
+      };
+      auto weight_at = [&](int i) -> double {
+        const float l = i < own ? src.at(s0 + i) : -CUDART_INF_F;
+        const bool in = l >= hi && (l > bv || (l == bv && base + s0 + i <= bi));
+        return sq_weight(in ? l : -CUDART_INF_F, r, sh->exp2_tab);
+      };
+      double b2 = before + __shfl_sync(0xffffffffu, warps_before, wid);
+      // the round: the first whose end passes the target, else the last
+      int i0 = 0;
+      for (int k = 0; k < own; k += 32 * SQ_ROUND) {
+        const int i = k + lane * SQ_ROUND;
+        const double own_r = i < own ? sh->rounds[wid][i / SQ_ROUND] : 0.0, z = scan(own_r);
+        const unsigned pass = __ballot_sync(0xffffffffu, own_r > 0.0 && b2 + z > aim);
+        if (pass) {
+          const int c = __ffs(pass) - 1;
+          i0 = k + c * SQ_ROUND;
+          b2 += __shfl_sync(0xffffffffu, z, c) - __shfl_sync(0xffffffffu, own_r, c);
+          break;
+        }
+        b2 += __shfl_sync(0xffffffffu, z, 31);
+      }
+      // its eight elements per lane, from another one in each lane: no bank twice
+      constexpr int EACH = SQ_ROUND / 32;
+      double x = 0.0;
+#pragma unroll 1
+      for (int j = 0; j < EACH; ++j) x += weight_at(i0 + EACH * lane + ((j + lane) & (EACH - 1)));
+      const double own_x = x;
+      x = scan(x);
+      const unsigned pass = __ballot_sync(0xffffffffu, own_x > 0.0 && b2 + x > aim);
+      int hit = -1;
+      double w_hit = 0.0;
+      bool sure = false;
+      if (pass) {   // (else the target is within rounding of the round's end: not sure)
+        const int c = __ffs(pass) - 1;
+        const double b3 = b2 + __shfl_sync(0xffffffffu, x, c) - __shfl_sync(0xffffffffu, own_x, c);
+        const double w = lane < EACH ? weight_at(i0 + EACH * c + lane) : 0.0, z = scan(w);
+        const unsigned over = __ballot_sync(0xffffffffu, w > 0.0 && b3 + z > aim);
+        if (over) {
+          const int h = __ffs(over) - 1;
+          hit = i0 + EACH * c + h;
+          const double after = b3 + __shfl_sync(0xffffffffu, z, h);
+          w_hit = __shfl_sync(0xffffffffu, w, h);
+          // both ends of the token's interval are clear of the target
+          sure = after - aim > eps && aim - (after - w_hit) > eps;
+        }
+      }
+      if (lane == 0) {
+        const bool good = hit >= 0 && sure;
+        if (good) {
+          a.token[t] = base + s0 + hit;
+          if (a.prob) a.prob[t] = (float)(w_hit / total);
+        }
+        push_all(&sh->push[4][0], SpPush{0.0, 0.0, 0.0f, good ? 0 : 1}, a.nc);
+      }
+    }
+  }
+  dense::cluster_sync();
+  return sh->push[4][0].bad == 0;
+}
+
+// The thread's largest and smallest logit of a slice, which goes into shared
+// memory on the way (RES), -inf behind its end.
+template <bool BF16, bool RES>
+__device__ void sp_load(const SpSrc<BF16, RES> &src, float *vals, int padded, float &mx, float &mn) {
+  const int tid = threadIdx.x;
+  mx = -CUDART_INF_F;
+  mn = CUDART_INF_F;
+  const SpSrc<BF16, false> mem{src.row, nullptr, src.n, src.vec};
+  constexpr int U = 8;
+  const int full = src.n / 4 * 4;
+  for (int i0 = 0; i0 < full; i0 += 4 * U * SP_THREADS) {
+    float4 q[U];
+#pragma unroll
+    for (int c = 0; c < U; ++c) {
+      const int i = i0 + 4 * (c * SP_THREADS + tid);
+      q[c] = i < full ? mem.four(i, full) : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+    }
+#pragma unroll
+    for (int c = 0; c < U; ++c) {
+      const int i = i0 + 4 * (c * SP_THREADS + tid);
+      if (i < full) {
+        mx = fmaxf(fmaxf(mx, fmaxf(q[c].x, q[c].y)), fmaxf(q[c].z, q[c].w));
+        mn = fminf(fminf(mn, fminf(q[c].x, q[c].y)), fminf(q[c].z, q[c].w));
+        if (RES) *reinterpret_cast<float4 *>(vals + i) = q[c];
+      }
+    }
+  }
+  for (int i = full + tid; i < src.n; i += SP_THREADS) {
+    const float v = mem.at(i);
+    mx = fmaxf(mx, v);
+    mn = fminf(mn, v);
+    if (RES) vals[i] = v;
+  }
+  if (RES)
+    for (int i = src.n + tid; i < padded; i += SP_THREADS) vals[i] = -CUDART_INF_F;
+}
+
+template <bool BF16, bool RES>
+__global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SpArgs a) {
   extern __shared__ __align__(16) uint8_t sp_smem[];
   SpShared *sh = reinterpret_cast<SpShared *>(sp_smem);
-  float *vals = reinterpret_cast<float *>(sp_smem + ((sizeof(SpShared) + 15) & ~(size_t)15));
+  float *stack = reinterpret_cast<float *>(sp_smem + sp_head_bytes());   // a round's logits per warp
+  float *vals = stack + SP_WARPS * SQ_ROUND;                             // RES: the slice
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int rank = (int)dense::cluster_rank(), t = blockIdx.x / a.nc;
+  const int rank = RES ? (int)dense::cluster_rank() : 0, t = blockIdx.x / a.nc;
   const int base = min(a.V, rank * a.slice), n = min(a.V, base + a.slice) - base;
 
   const float temp = a.temperature ? a.temperature[t] : 1.0f;
@@ -419,52 +1164,31 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SpArgs a) {
   const float min_p = a.min_p ? a.min_p[t] : 0.0f;
   const float u = a.u[t];
 
-  // the slice into shared memory, NaN as -inf
-  float mx = -CUDART_INF_F;
-  auto put = [&](int i, float v) {
-    v = v == v ? v : -CUDART_INF_F;
-    vals[i] = v;
-    mx = fmaxf(mx, v);
-  };
-  const size_t row = (size_t)t * a.ld + base;
-  if (BF16) {
-    const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(a.logits) + row;
-    const int nv = (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? n / 8 : 0;
-    for (int i = tid; i < nv; i += SP_THREADS) {
-      const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        put(8 * i + 2 * j, __uint_as_float(w[j] << 16));
-        put(8 * i + 2 * j + 1, __uint_as_float(w[j] & 0xffff0000u));
-      }
-    }
-    for (int i = 8 * nv + tid; i < n; i += SP_THREADS) put(i, __bfloat162float(p[i]));
-  } else {
-    const float *p = static_cast<const float *>(a.logits) + row;
-    const int nv = (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? n / 4 : 0;
-    for (int i = tid; i < nv; i += SP_THREADS) {
-      const float4 q = __ldcs(reinterpret_cast<const float4 *>(p) + i);
-      put(4 * i, q.x);
-      put(4 * i + 1, q.y);
-      put(4 * i + 2, q.z);
-      put(4 * i + 3, q.w);
-    }
-    for (int i = 4 * nv + tid; i < n; i += SP_THREADS) put(i, p[i]);
-  }
-  int par = 0;
+  const void *row = static_cast<const uint8_t *>(a.logits) + ((size_t)t * a.ld + base) * (BF16 ? 2 : 4);
+  const SpSrc<BF16, RES> src{row, vals, n, (reinterpret_cast<uintptr_t>(row) & (BF16 ? 7 : 15)) == 0};
+  float mx, mn;
+  sp_load(src, vals, SP_WARPS * a.seg, mx, mn);
   mx = warp_max(mx);
-  if (lane == 0) sh->warp_f[0][wid] = mx;
+  mn = -warp_max(-mn);
+  if (lane == 0) {
+    sh->warp_f[0][wid] = mx;
+    sh->warp_f[1][wid] = mn;
+  }
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 0; w < SP_WARPS; ++w) mx = fmaxf(mx, sh->warp_f[0][w]);
-    sh->part[par].max_in = mx;
+  if (wid == 0) {
+    mx = warp_max(sh->warp_f[0][lane % SP_WARPS]);
+    mn = -warp_max(-sh->warp_f[1][lane % SP_WARPS]);
+    if (lane == 0) push_all(&sh->push[6][rank], SpPush{(double)mx, (double)mn, 0.0f, 0}, a.nc);
   }
   dense::cluster_sync();
   SpRow r;
   r.max = -CUDART_INF_F;
-  for (int c = 0; c < a.nc; ++c) r.max = fmaxf(r.max, dense::peer(&sh->part[par], c)->max_in);
-  par ^= 1;
+  mn = CUDART_INF_F;
+  for (int c = 0; c < a.nc; ++c) {
+    r.max = fmaxf(r.max, (float)sh->push[6][c].a);
+    mn = fminf(mn, (float)sh->push[6][c].b);
+  }
+  int par = 0;
   r.temp = (double)temp;
   r.bv = -CUDART_INF_F;
   r.bi = a.V;
@@ -484,7 +1208,7 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SpArgs a) {
   if (temp == 0.0f) {   // greedy: the lowest index of the largest logit
     int at = 0x7fffffff;
     for (int i = tid; i < n; i += SP_THREADS)
-      if (vals[i] == r.max) at = min(at, base + i);
+      if (src.at(i) == r.max) at = min(at, base + i);
     at = __reduce_min_sync(0xffffffffu, at);
     if (lane == 0) sh->warp_i[wid] = at;
     __syncthreads();
@@ -501,18 +1225,22 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SpArgs a) {
     dense::cluster_sync();
     return;
   }
+  if (r.max < CUDART_INF_F) {
+    if (sq_row<BF16, RES>(src, stack, base, r.max, mn, temp, top_k, top_p, min_p, u, sh, a, t, rank)) return;
+    dense::cluster_sync();
+  }
   if (tid == 0) sh->live = sp_live(r, min_p > 0.0f ? fmax((double)min_p, SP_W_MIN) : SP_W_MIN);
   __syncthreads();
   r.live = sh->live;
 
-  if (top_k > 0 && top_k < a.V) sp_select<true>(vals, n, base, r, (double)top_k, sh, a, rank, par);
+  if (top_k > 0 && top_k < a.V) sp_select<true>(src, n, base, r, (double)top_k, sh, a, rank, par);
   if (top_p < 1.0f) {
     double s = 0.0;
     for (int i = tid; i < n; i += SP_THREADS)
-      if (sp_kept(vals[i], base + i, r)) s += sp_weight(vals[i], r);
+      if (sp_kept(src.at(i), base + i, r)) s += sp_weight(src.at(i), r);
     s = sp_cluster_sum(s, sh, a, par);
     // (at least the smallest weight: top_p <= 0 keeps the first rank)
-    sp_select<false>(vals, n, base, r, fmax(SP_W_MIN, (double)top_p * s), sh, a, rank, par);
+    sp_select<false>(src, n, base, r, fmax(SP_W_MIN, (double)top_p * s), sh, a, rank, par);
   }
 
   // the token, by index: sums per warp segment, per CTA, over the cluster
@@ -520,7 +1248,7 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SpArgs a) {
   const int s0 = wid * seg, s1 = min(n, s0 + seg);
   double ws = 0.0;
   for (int i = s0 + lane; i < s1; i += 32)
-    if (sp_kept(vals[i], base + i, r)) ws += sp_weight(vals[i], r);
+    if (sp_kept(src.at(i), base + i, r)) ws += sp_weight(src.at(i), r);
   ws = warp_sum_d(ws);
   if (lane == 0) sh->warp_d[1][wid] = ws;
   __syncthreads();
@@ -558,7 +1286,7 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SpArgs a) {
       int hit = -1, lastk = -1;
       for (int i0 = s0; i0 < s1 && hit < 0; i0 += 32) {
         const int i = i0 + lane;
-        double x = i < s1 && sp_kept(vals[i], base + i, r) ? sp_weight(vals[i], r) : 0.0;
+        double x = i < s1 && sp_kept(src.at(i), base + i, r) ? sp_weight(src.at(i), r) : 0.0;
         const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
         const bool mine = x > 0.0;
 #pragma unroll
@@ -574,7 +1302,7 @@ __global__ void __launch_bounds__(SP_THREADS) sample_kernel(SpArgs a) {
       if (hit < 0) hit = lastk;
       if (lane == 0) {
         a.token[t] = base + hit;
-        if (a.prob) a.prob[t] = (float)(sp_weight(vals[hit], r) / total);
+        if (a.prob) a.prob[t] = (float)(sp_weight(src.at(hit), r) / total);
       }
     }
   }
@@ -599,14 +1327,19 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
                        reinterpret_cast<uintptr_t>(prob) | reinterpret_cast<uintptr_t>(dev_status);
   if ((a4 & 3) || !aligned16(logits)) return QMOE_ERR_INVALID_ARG;
   if (V > SP_MAX_V || T > (1 << 27)) return QMOE_ERR_UNSUPPORTED;
+  // many rows: one CTA each; few rows: enough CTAs to hold a row, then enough to fill the machine
+  const int sms = num_sms();
+  const bool res = T < sms / 2 && V <= SP_MAX_CLUSTER * SP_MAX_SLICE;
   int nc = 1;
-  // enough CTAs to hold the row, then enough to fill the machine
-  while (nc < SP_MAX_CLUSTER && ((V + nc - 1) / nc > SP_MAX_SLICE / 3 || (long long)T * nc * 2 <= num_sms())) nc *= 2;
+  if (res)
+    while (nc < SP_MAX_CLUSTER && ((V + nc - 1) / nc > SP_MAX_SLICE / 2 || (long long)T * nc * 2 <= sms)) nc *= 2;
   const int slice = ((V + nc - 1) / nc + 7) / 8 * 8;
-  const size_t smem = ((sizeof(SpShared) + 15) & ~(size_t)15) + (size_t)slice * 4;
+  const int seg = (slice + SP_WARPS * 128 - 1) / (SP_WARPS * 128) * 128;
+  const size_t smem = sp_head_bytes() + (size_t)SP_WARPS * (SQ_ROUND + (res ? seg : 0)) * 4;
   if (smem > max_smem_optin()) return QMOE_ERR_UNSUPPORTED;
-  SpArgs args{logits, temperature, top_p, min_p, u, top_k, token, prob, dev_status, ld, T, V, slice, nc};
-  const void *fn = dtype == QMOE_BF16 ? (const void *)sample_kernel<true> : (const void *)sample_kernel<false>;
+  SpArgs args{logits, temperature, top_p, min_p, u, top_k, token, prob, dev_status, ld, T, V, slice, nc, seg};
+  const void *fn = dtype == QMOE_BF16 ? (res ? (const void *)sample_kernel<true, true> : (const void *)sample_kernel<true, false>)
+                                      : (res ? (const void *)sample_kernel<false, true> : (const void *)sample_kernel<false, false>);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return QMOE_ERR_CUDA;
   void *params[] = {&args};
