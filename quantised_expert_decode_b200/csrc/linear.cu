@@ -14,8 +14,11 @@
 //     A warp's lanes then hold neighbouring features of one token, so results
 //     leave in coalesced rows of any alignment, and few tokens waste little:
 //     decode and verify batches, and outputs whose rows are not 16-byte aligned.
-//   tokens   - the 128 rows are tokens, a thread holds 32 neighbouring features
-//     of its token per load and writes them with 16-byte stores: large batches.
+//   tokens   - the 128 rows are tokens, a thread holds 16 neighbouring features
+//     of its token: large batches. Results leave through shared memory, 32 rows
+//     of 128 bytes per warp and TMA store, and the residual comes the same way a
+//     step ahead: written straight from the lanes, every 16 bytes of a warp's
+//     store lie in another row, and the epilogue took twice the products' time.
 //   pairs    - tokens, with two CTAs on one tile of 256 x 256: each loads 128
 //     rows of either operand, half of what it would load alone, since the loads
 //     from L2 bound the lone CTA (48 KB a step against 32 KB).
@@ -37,12 +40,12 @@ namespace {
 constexpr int LN_ROWS = 128;                     // rows of the A operand per CTA (MMA M)
 constexpr int LN_KB = 128;                       // bytes of K per pipeline step
 constexpr int LN_A_BYTES = LN_ROWS * LN_KB;      // 16 KB
-constexpr int LN_W_TMA = 0, LN_W_MMA = 1, LN_W_EPI = 4, LN_N_EPI = 8;
-constexpr int LN_THREADS = 32 * (LN_W_EPI + LN_N_EPI);
+constexpr int LN_W_TMA = 0, LN_W_MMA = 1, LN_W_EPI = 2;
 constexpr int LN_MAX_STAGES = 10;
 constexpr int LN_MAX_SPLIT = 8;
 constexpr int LN_MAX_K = 65536;                  // keeps |int32 sums| below 2^31
-constexpr int LN_SMEM = 200 * 1024;              // ring budget
+constexpr int LN_SMEM = 224 * 1024;              // ring and staging
+constexpr int LN_BOX = 4096;                     // staging: 32 rows of 128 bytes
 constexpr int LN_GROUP = 8;                      // A tiles that share B tiles in L2
 constexpr int LN_SEG = 4;                        // steps per accumulator slot of fp32 results
 
@@ -51,12 +54,14 @@ enum { LN_FEATURES, LN_TOKENS, LN_PAIRS };
 struct LnBars {
   uint64_t full[LN_MAX_STAGES], empty[LN_MAX_STAGES];
   uint64_t acc_full[2], acc_empty[2], fin;
+  uint64_t res_full[16];
   uint32_t tmem_base;
   int abort;
 };
 
 struct LnArgs {
   CUtensorMap tm_a, tm_b;        // the 128-row operand and the BT-row operand
+  CUtensorMap tm_out, tm_res;    // tokens, pairs: 32 rows of 128 bytes
   const float *s_a, *s_w;        // per token, per feature (8-bit operands), or null
   const float *bias;             // [N] or null
   const void *res;               // [M, N] like out, or null
@@ -70,14 +75,21 @@ struct LnArgs {
   int32_t *status;
 };
 
+// Epilogue warps: four per 32-lane quarter of the widest tiles, else two.
+__host__ __device__ constexpr int ln_epi_warps(int mode, int BT) { return mode == LN_PAIRS && BT == 256 ? 16 : 8; }
+__host__ __device__ constexpr int ln_threads(int mode, int BT) { return 32 * (LN_W_EPI + ln_epi_warps(mode, BT)); }
+// Staging boxes: 16 in all, so one or two per warp.
+__host__ __device__ constexpr int ln_boxes(int mode) { return mode == LN_FEATURES ? 0 : 16; }
 // Rows of the B operand that one CTA loads.
 __host__ __device__ constexpr int ln_b_rows(int mode, int BT) { return mode == LN_PAIRS ? BT / 2 : BT; }
 __host__ __device__ constexpr int ln_stage_bytes(int mode, int BT) { return LN_A_BYTES + ln_b_rows(mode, BT) * LN_KB; }
 __host__ __device__ constexpr int ln_stages(int mode, int BT) {
-  return LN_SMEM / ln_stage_bytes(mode, BT) < LN_MAX_STAGES ? LN_SMEM / ln_stage_bytes(mode, BT) : LN_MAX_STAGES;
+  return (LN_SMEM - ln_boxes(mode) * LN_BOX) / ln_stage_bytes(mode, BT) < LN_MAX_STAGES
+             ? (LN_SMEM - ln_boxes(mode) * LN_BOX) / ln_stage_bytes(mode, BT)
+             : LN_MAX_STAGES;
 }
 constexpr int ln_smem_bytes(int mode, int BT) {
-  return 1024 + ln_stages(mode, BT) * ln_stage_bytes(mode, BT) + (int)sizeof(LnBars);
+  return 1024 + ln_stages(mode, BT) * ln_stage_bytes(mode, BT) + ln_boxes(mode) * LN_BOX + (int)sizeof(LnBars);
 }
 // TMEM columns of the two accumulator slots: a power of two of at least 32
 __host__ __device__ constexpr int ln_tmem_cols(int BT) { return 2 * BT < 32 ? 32 : 2 * BT; }
@@ -120,11 +132,28 @@ __device__ __forceinline__ void ln_krange(const LnArgs &a, int rank, int &k0, in
   k1 = (int)((long long)a.ksteps * (rank + 1) / a.split);
 }
 
-// silu by the hardware exponential and quotient (relative error below 1e-6
-// around the origin, where the values are), gelu by erfc, which keeps the
-// negative tail's relative precision. One copy of erfc's code, called: inlined
-// into every unrolled element it does not fit the instruction cache.
-__device__ __noinline__ float ln_gelu(float v) { return 0.5f * v * erfcf(-0.70710678f * v); }
+// silu by the hardware exponential and quotient: relative error below 1e-6
+// around the origin, where the values are. gelu = v erfc(-v / sqrt 2) / 2 with
+// the Chebyshev fit of erfc in Numerical Recipes (W. H. Press et al., "erfcc",
+// relative error below 1.2e-7 of its own), which keeps the negative tail's
+// relative precision; CUDA's erfcf costs three times the instructions, and the
+// epilogue of 4096 x 4096 values with it took longer than the products.
+__device__ __forceinline__ float ln_gelu(float v) {
+  const float x = -0.70710678118654752f * v, z = fabsf(x);
+  const float t = __fdividef(1.0f, __fmaf_rn(0.5f, z, 1.0f));
+  float p = 0.17087277f;
+  p = __fmaf_rn(p, t, -0.82215223f);
+  p = __fmaf_rn(p, t, 1.48851587f);
+  p = __fmaf_rn(p, t, -1.13520398f);
+  p = __fmaf_rn(p, t, 0.27886807f);
+  p = __fmaf_rn(p, t, -0.18628806f);
+  p = __fmaf_rn(p, t, 0.09678418f);
+  p = __fmaf_rn(p, t, 0.37409196f);
+  p = __fmaf_rn(p, t, 1.00002368f);
+  p = __fmaf_rn(p, t, -1.26551223f);
+  const float e = t * __expf(__fmaf_rn(-z, z, p));   // erfc(|x|)
+  return 0.5f * v * (x >= 0.0f ? e : 2.0f - e);
+}
 __device__ __forceinline__ float ln_relu(float v) { return v > 0.0f ? v : (v == v ? 0.0f : v); }
 __device__ __forceinline__ float ln_silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
@@ -145,6 +174,11 @@ __device__ __forceinline__ void ln_act_all(float (&v)[W], int act) {
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = ln_gelu(v[i]);
   }
+}
+
+// Brings a 32-byte sector into L1.
+__device__ __forceinline__ void touch(const float *p) {
+  asm volatile("{ .reg .f32 t; ld.global.nc.f32 t, [%0]; }" ::"l"(p));
 }
 
 template <bool I8>
@@ -188,72 +222,55 @@ __device__ __forceinline__ void ln_out_features(const LnArgs &a, float (&v)[16],
     if (i < mn) ln_store(a.out, (long long)(m0 + i) * a.ldo + n, a.out_f32, v[i]);
 }
 
-// Residual values of W neighbouring features of a token, as stored.
-template <int W>
-struct LnRes {
-  uint4 q[W / 4];
-};
-template <int W>
-__device__ __forceinline__ void ln_load_res(const LnArgs &a, LnRes<W> &r, int m, int n0) {
-  if (!a.res || m >= a.M || n0 + W > a.N) return;
-  const long long at = (long long)m * a.ldr + n0;
-  const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.res) + at * (a.out_f32 ? 4 : 2));
+// Epilogue of 16 neighbouring features (from n0) of the lane's token, into its
+// row of a staging box (16-byte chunks from `chunk` on, each at chunk ^ (row % 8),
+// the 128-byte swizzle), where the residual already lies.
+template <bool I8>
+__device__ __forceinline__ void ln_stage_tokens(const LnArgs &a, float (&v)[16], int n0, float sa, uint8_t *row, int chunk) {
+  const int swz = threadIdx.x & 7;
+  if (n0 + 16 <= a.N) {
 #pragma unroll
-  for (int j = 0; j < W / 8; ++j) r.q[j] = p[j];
-  if (a.out_f32)
-#pragma unroll
-    for (int j = W / 8; j < W / 4; ++j) r.q[j] = p[j];
-}
-
-// Epilogue of W neighbouring features (from n0) of token m.
-template <bool I8, int W>
-__device__ __forceinline__ void ln_out_tokens(const LnArgs &a, float (&v)[W], int m, int n0, float sa, const LnRes<W> &res) {
-  if (m >= a.M) return;
-  if (n0 + W > a.N) {
-    for (int i = 0; i < W; ++i)
-      if (n0 + i < a.N) {
-        float x = v[0];   // v is indexed at compile time only
-#pragma unroll
-        for (int j = 1; j < W; ++j) x = j == i ? v[j] : x;
-        ln_finish<I8>(a, x, m, n0 + i, I8 ? __ldg(a.s_w + n0 + i) : 1.0f, a.bias ? __ldg(a.bias + n0 + i) : 0.0f);
-      }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < W / 4; ++j) {
-    const float4 sw = I8 ? __ldg(reinterpret_cast<const float4 *>(a.s_w + n0) + j) : make_float4(1.f, 1.f, 1.f, 1.f);
-    const float4 bb = a.bias ? __ldg(reinterpret_cast<const float4 *>(a.bias + n0) + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-    v[4 * j] = ln_acc<I8>(v[4 * j], sa, sw.x) + bb.x;
-    v[4 * j + 1] = ln_acc<I8>(v[4 * j + 1], sa, sw.y) + bb.y;
-    v[4 * j + 2] = ln_acc<I8>(v[4 * j + 2], sa, sw.z) + bb.z;
-    v[4 * j + 3] = ln_acc<I8>(v[4 * j + 3], sa, sw.w) + bb.w;
-  }
-  ln_act_all(v, a.act);
-  const long long oo = (long long)m * a.ldo + n0;
-  if (a.out_f32) {
-    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + oo);
-#pragma unroll
-    for (int j = 0; j < W / 4; ++j) {
-      float4 x = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-      if (a.res) {
-        const uint4 q = res.q[j];
-        x.x += __uint_as_float(q.x);
-        x.y += __uint_as_float(q.y);
-        x.z += __uint_as_float(q.z);
-        x.w += __uint_as_float(q.w);
-      }
-      o[j] = x;
+    for (int j = 0; j < 4; ++j) {
+      const float4 sw = I8 ? __ldg(reinterpret_cast<const float4 *>(a.s_w + n0) + j) : make_float4(1.f, 1.f, 1.f, 1.f);
+      const float4 bb = a.bias ? __ldg(reinterpret_cast<const float4 *>(a.bias + n0) + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[4 * j] = ln_acc<I8>(v[4 * j], sa, sw.x) + bb.x;
+      v[4 * j + 1] = ln_acc<I8>(v[4 * j + 1], sa, sw.y) + bb.y;
+      v[4 * j + 2] = ln_acc<I8>(v[4 * j + 2], sa, sw.z) + bb.z;
+      v[4 * j + 3] = ln_acc<I8>(v[4 * j + 3], sa, sw.w) + bb.w;
     }
   } else {
-    uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + oo);
 #pragma unroll
-    for (int j = 0; j < W / 8; ++j) {
+    for (int j = 0; j < 16; ++j) {
+      const int n = min(n0 + j, a.N - 1);   // (what lies past N is not stored)
+      v[j] = ln_acc<I8>(v[j], sa, I8 ? __ldg(a.s_w + n) : 1.0f) + (a.bias ? __ldg(a.bias + n) : 0.0f);
+    }
+  }
+  ln_act_all(v, a.act);
+  if (a.out_f32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float4 *p = reinterpret_cast<float4 *>(row + (((chunk + j) ^ swz) << 4));
+      float4 x = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      if (a.res) {
+        const float4 r = *p;
+        x.x += r.x;
+        x.y += r.y;
+        x.z += r.z;
+        x.w += r.w;
+      }
+      *p = x;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint4 *p = reinterpret_cast<uint4 *>(row + (((chunk + j) ^ swz) << 4));
       uint32_t rw[4] = {0, 0, 0, 0}, ow[4];
       if (a.res) {
-        rw[0] = res.q[j].x;
-        rw[1] = res.q[j].y;
-        rw[2] = res.q[j].z;
-        rw[3] = res.q[j].w;
+        const uint4 r = *p;
+        rw[0] = r.x;
+        rw[1] = r.y;
+        rw[2] = r.z;
+        rw[3] = r.w;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -265,21 +282,23 @@ __device__ __forceinline__ void ln_out_tokens(const LnArgs &a, float (&v)[W], in
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         ow[i] = *reinterpret_cast<const uint32_t *>(&h);
       }
-      o[j] = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+      *p = make_uint4(ow[0], ow[1], ow[2], ow[3]);
     }
   }
 }
 
 // SEG: a slot holds LN_SEG steps, and the epilogue's threads add the slots.
 template <int MODE, int BT, bool I8, bool SEG>
-__global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_constant__ LnArgs a) {
+__global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const __grid_constant__ LnArgs a) {
   extern __shared__ uint8_t ln_smem[];
   constexpr bool FEATURES = MODE == LN_FEATURES, PAIRS = MODE == LN_PAIRS;
   constexpr int STAGES = ln_stages(MODE, BT), STAGE = ln_stage_bytes(MODE, BT), BROWS = ln_b_rows(MODE, BT);
   constexpr int CTAS = PAIRS ? 2 : 1;                       // CTAs on one tile
-  constexpr int EPI_COLS = BT < 32 ? BT : BT / 2;           // columns of an epilogue warp
+  constexpr int N_EPI = ln_epi_warps(MODE, BT), THREADS = ln_threads(MODE, BT);
+  constexpr int EPI_COLS = BT < 32 ? BT : BT / (N_EPI / 4);  // columns of an epilogue warp
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ln_smem) + 1023) & ~(uintptr_t)1023);
-  LnBars *b = reinterpret_cast<LnBars *>(sm + STAGES * STAGE);
+  uint8_t *boxes = sm + STAGES * STAGE;
+  LnBars *b = reinterpret_cast<LnBars *>(boxes + ln_boxes(MODE) * LN_BOX);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIRS || a.split > 1 ? (int)dense::cluster_rank() : 0;
   if (threadIdx.x == 0) {
@@ -289,8 +308,9 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b->acc_full[i], 1);
-      mbar_init(&b->acc_empty[i], CTAS * LN_N_EPI);
+      mbar_init(&b->acc_empty[i], CTAS * N_EPI);
     }
+    for (int i = 0; i < 16; ++i) mbar_init(&b->res_full[i], 1);
     mbar_init(&b->fin, 1);
     b->abort = 0;
     fence_mbar_init();
@@ -408,34 +428,38 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
     }
     if (!mbar_wait(&b->fin, 0, clock64() + WAIT_BUDGET_CYCLES * (PAIRS && rank ? 2 : 1))) set_status(a.status, DEV_TIMEOUT);
   } else if (warp >= LN_W_EPI && (PAIRS || a.split == 1)) {
-    const int w = warp - LN_W_EPI, q = w & 3, half = w >> 2;
-    const int col0 = BT < 32 ? 0 : half * EPI_COLS;
-    const bool works = BT >= 32 || half == 0;
+    const int w = warp - LN_W_EPI, q = warp & 3, part = w >> 2;   // (a warp reads the TMEM lanes of its number mod 4)
+    const int col0 = BT < 32 ? 0 : part * EPI_COLS;
+    const bool works = BT >= 32 || part == 0;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t empty0 = PAIRS ? dense::peer_addr(&b->acc_empty[0], 0) : 0;
-    uint32_t c = 0;
+    uint32_t c = 0;   // accumulator slots read
     bool ok = true;
-    for (int i = first; i < ntiles && ok; i += step) {
-      int ta, tb;
-      ln_tile(a, i, ta, tb);
-      const int row = ta * a_row + (PAIRS ? rank * LN_ROWS : 0) + q * 32 + lane;   // feature, or token
-      const int colb = tb * BT + col0;
-      auto release = [&](int slot) {
-        tc05::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIRS) dense::mbar_arrive_peer(empty0 + slot * 8);
-          else mbar_arrive(&b->acc_empty[slot]);
-        }
-      };
-      if constexpr (FEATURES) {
-        constexpr int NCH = EPI_COLS / 16;
+    auto wait_slot = [&](int slot) {
+      const bool good = ln_wait_warp(&b->acc_full[slot], (c >> 1) & 1, b, a.status);
+      tc05::fence_after_sync();
+      return good;
+    };
+    auto release = [&](int slot) {
+      tc05::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIRS) dense::mbar_arrive_peer(empty0 + slot * 8);
+        else mbar_arrive(&b->acc_empty[slot]);
+      }
+      ++c;
+    };
+    if constexpr (FEATURES) {
+      constexpr int NCH = EPI_COLS / 16;
+      for (int i = first; i < ntiles && ok; i += step) {
+        int ta, tb;
+        ln_tile(a, i, ta, tb);
+        const int n = ta * LN_ROWS + q * 32 + lane, m0 = tb * BT + col0;
         float v[NCH][16];
-        for (int sg = 0; sg < segs && ok; ++sg, ++c) {
+        for (int sg = 0; sg < segs; ++sg) {
           const int slot = c & 1;
-          ok = ln_wait_warp(&b->acc_full[slot], (c >> 1) & 1, b, a.status);
+          ok = wait_slot(slot);
           if (!ok) break;
-          tc05::fence_after_sync();
           if (works) {
 #pragma unroll
             for (int h = 0; h < NCH; ++h) {
@@ -449,55 +473,135 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         }
         if (ok && works)
 #pragma unroll
-          for (int h = 0; h < NCH; ++h) ln_out_features<I8>(a, v[h], row, colb + 16 * h);
-      } else {
-        const float sa = I8 && row < a.M ? __ldg(a.s_a + row) : 1.0f;
+          for (int h = 0; h < NCH; ++h) ln_out_features<I8>(a, v[h], n, m0 + 16 * h);
+        __syncwarp();
+      }
+    } else {
+      // the warp's staging boxes in turn: box (column group) by box through all
+      // tiles, the residual of the next box loaded while this one is formed
+      constexpr int NBOX = 16 / N_EPI;
+      const int es = a.out_f32 ? 4 : 2, bcols = 128 / es, ngroups = EPI_COLS / bcols;
+      uint8_t *box0 = boxes + w * NBOX * LN_BOX;
+      uint64_t *rbar = &b->res_full[w * NBOX];
+      uint32_t n_used = 0;         // boxes stored so far
+      struct Tile {
+        int m, n;   // the warp's first row and column
+      };
+      auto tile_at = [&](int i) {
+        int ta, tb;
+        ln_tile(a, i, ta, tb);
+        return Tile{ta * a_row + (PAIRS ? rank * LN_ROWS : 0) + q * 32, tb * BT + col0};
+      };
+      // (lane 0, once the box's last store has been read; nothing past the matrix)
+      auto load_res = [&](int m, int n, uint32_t k) {
+        if (m >= a.M || n >= a.N) return false;
+        mbar_arrive_expect_tx(&rbar[k % NBOX], LN_BOX);
+        dense::tma_load_2d(box0 + k % NBOX * LN_BOX, &a.tm_res, n, m, &rbar[k % NBOX]);
+        return true;
+      };
+      uint32_t phase[NBOX] = {};   // residual loads waited for, per box
+      bool pending = false;        // box n_used has a residual under way
+      Tile next = tile_at(first);
+      if (a.res && lane == 0) pending = load_res(next.m, next.n, 0);
+      pending = __shfl_sync(0xffffffffu, pending, 0);
+      for (int i = first; i < ntiles && ok; i += step) {
+        constexpr int NCH = EPI_COLS / 16;
+        float acc[SEG ? NCH : 1][16];
+        const Tile here = next;
+        const bool last_tile = i + step >= ntiles;
+        next = tile_at(last_tile ? i : i + step);
+        const float sa = I8 && here.m + lane < a.M ? __ldg(a.s_a + here.m + lane) : 1.0f;
+        // the columns' bias and scales into L1 while the products run: every 16
+        // columns would wait for them otherwise
+        for (int n = here.n + 8 * lane; n < min(a.N, here.n + EPI_COLS); n += 256) {
+          if (a.bias) touch(a.bias + n);
+          if (I8) touch(a.s_w + n);
+        }
+        int slot = c & 1;
         if constexpr (SEG) {
-          constexpr int NCH = EPI_COLS / 16;
-          float v[NCH][16];
-          for (int sg = 0; sg < segs && ok; ++sg, ++c) {
-            const int slot = c & 1;
-            ok = ln_wait_warp(&b->acc_full[slot], (c >> 1) & 1, b, a.status);
+          for (int sg = 0; sg < segs; ++sg) {
+            slot = c & 1;
+            ok = wait_slot(slot);
             if (!ok) break;
-            tc05::fence_after_sync();
 #pragma unroll
             for (int h = 0; h < NCH; ++h) {
               float x[16];
               tc05::ld16(tmem + slot * BT + lanes + col0 + 16 * h, x);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[h][j] = sg == 0 ? x[j] : __fadd_rn(v[h][j], x[j]);
+              for (int j = 0; j < 16; ++j) acc[h][j] = sg == 0 ? x[j] : __fadd_rn(acc[h][j], x[j]);
             }
             release(slot);
           }
-          if (ok)
-#pragma unroll
-            for (int h = 0; h < NCH; ++h) {
-              LnRes<16> res;
-              ln_load_res(a, res, row, colb + 16 * h);
-              ln_out_tokens<I8>(a, v[h], row, colb + 16 * h, sa, res);
-            }
         } else {
-          constexpr int NCH = EPI_COLS / 32;
-          LnRes<32> res, next;
-          ln_load_res(a, next, row, colb);   // under way while the tile's products run
-          const int slot = c & 1;
-          ok = ln_wait_warp(&b->acc_full[slot], (c >> 1) & 1, b, a.status);
-          if (!ok) break;
-          tc05::fence_after_sync();
-#pragma unroll 1
-          for (int h = 0; h < NCH; ++h) {
-            res = next;
-            if (h + 1 < NCH) ln_load_res(a, next, row, colb + 32 * (h + 1));
-            float v[32];
-            __syncwarp();
-            dense::tmem_ld32(tmem + slot * BT + lanes + col0 + 32 * h, v);
-            if (h + 1 == NCH) release(slot);
-            ln_out_tokens<I8>(a, v, row, colb + 32 * h, sa, res);
-          }
-          ++c;
+          ok = wait_slot(slot);
         }
-        __syncwarp();
+        if (!ok) break;
+        auto one_box = [&](int g, auto values) {   // values(h): 16 columns of the group
+          const int m0 = here.m, n0 = here.n + g * bcols;
+          const bool live = m0 < a.M && n0 < a.N;
+          const uint32_t k = n_used % NBOX;
+          uint8_t *box = box0 + k * LN_BOX;
+          if (live && a.res) {
+            uint32_t ph = phase[0];
+            if (NBOX > 1 && k == 1) ph = phase[NBOX - 1];
+            ok = ln_wait_warp(&rbar[k], ph & 1, b, a.status);
+            if (k == 0) ++phase[0];
+            else ++phase[NBOX - 1];
+          } else if (live) {
+            if (lane == 0) dense::store_wait_read<NBOX - 1>();
+            __syncwarp();
+          }
+          pending = false;
+          if (!ok) return;
+          if (live) {
+            values(box + lane * 128, n0);
+            tc05::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) dense::tma_store_2d(&a.tm_out, n0, m0, box);
+            ++n_used;
+          }
+          if (a.res) {
+            // the next box: of this tile or of the next
+            const bool more = g + 1 < ngroups;
+            if (lane == 0 && (more || !last_tile)) {
+              dense::store_wait_read<NBOX - 1>();
+              pending = load_res(more ? m0 : next.m, more ? n0 + bcols : next.n, n_used);
+            }
+            pending = __shfl_sync(0xffffffffu, pending, 0);
+          }
+        };
+        if constexpr (SEG) {   // fp32: a box is 32 columns
+#pragma unroll
+          for (int g = 0; g < EPI_COLS / 32; ++g)
+            one_box(g, [&](uint8_t *row, int n0) {
+              ln_stage_tokens<I8>(a, acc[2 * g], n0, sa, row, 0);
+              ln_stage_tokens<I8>(a, acc[2 * g + 1], n0 + 16, sa, row, 4);
+            });
+        } else {
+#pragma unroll 1
+          for (int g = 0; g < ngroups; ++g)
+            one_box(g, [&](uint8_t *row, int n0) {
+#pragma unroll 1
+              for (int h = 0; h < bcols / 32; ++h) {
+                const uint32_t from = tmem + slot * BT + lanes + col0 + g * bcols + 32 * h;
+                float v[16], v2[16];
+                __syncwarp();
+                tc05::ld16x2(from, from + 16, v, v2);
+                ln_stage_tokens<I8>(a, v, n0 + 32 * h, sa, row, 2 * h * es);
+                ln_stage_tokens<I8>(a, v2, n0 + 32 * h + 16, sa, row, (2 * h + 1) * es);
+              }
+            });
+          release(slot);
+        }
       }
+      // a residual load that nobody waited for (after an error) still lands
+      if (pending && lane == 0) {
+        const uint32_t k = n_used % NBOX;
+        if (!mbar_wait(&rbar[k], (k == 0 ? phase[0] : phase[NBOX - 1]) & 1, clock64() + WAIT_BUDGET_CYCLES))
+          set_status(a.status, DEV_TIMEOUT);
+      }
+      if (lane == 0) dense::store_wait_all();
+      __syncwarp();
     }
   }
   __syncwarp();
@@ -511,7 +615,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
       int ta, tb;
       ln_tile(a, first, ta, tb);
       float *xch = reinterpret_cast<float *>(sm);
-      const int w = warp - LN_W_EPI, q = w & 3, half = w >> 2, f = q * 32 + lane;
+      const int w = warp - LN_W_EPI, q = warp & 3, half = w >> 2, f = q * 32 + lane;
       const int col0 = BT < 32 ? 0 : half * EPI_COLS;
       constexpr int NCH = EPI_COLS / 16;
       float v[NCH][16];
@@ -548,7 +652,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
       __syncwarp();
       dense::cluster_sync();
       const int m0 = tb * BT, mn = min(BT, a.M - m0), n0 = ta * LN_ROWS + rank * fl;
-      for (int i = threadIdx.x; i < mn * fl; i += LN_THREADS) {
+      for (int i = threadIdx.x; i < mn * fl; i += THREADS) {
         const int m = i / fl, fi = i - m * fl, n = n0 + fi;
         if (n >= a.N) continue;
         float acc;
@@ -576,34 +680,39 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- host side --
-// [rows][K] with row stride ld (elements), boxes of box_rows x 128 bytes in the
-// 128-byte swizzle.
-bool ln_map(CUtensorMap *m, const void *base, bool i8, int K, int rows, long long ld, int box_rows) {
+// [rows][cols] with row stride ld (elements) of 1, 2 or 4 bytes, boxes of
+// box_rows x 128 bytes in the 128-byte swizzle.
+bool ln_map(CUtensorMap *m, const void *base, int es, int cols, int rows, long long ld, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = dense::tensor_map_encoder();
   if (!enc) return false;
-  const int es = i8 ? 1 : 2;
-  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * es};
-  const cuuint32_t box[2] = {(cuuint32_t)(LN_KB / es), (cuuint32_t)box_rows};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
   const cuuint32_t st[2] = {1, 1};
-  return enc(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
-             dims, strides, box, st, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(m,
+             es == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+             : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+             2, const_cast<void *>(base), dims, strides, box, st, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int MODE, int BT>
 const void *ln_kernel(bool i8, bool f32) {
   if (i8) return (const void *)linear_kernel<MODE, BT, true, false>;
-  return f32 ? (const void *)linear_kernel<MODE, BT, false, true> : (const void *)linear_kernel<MODE, BT, false, false>;
+  // (fp32 results from wide pairs: a thread's sums do not fit its registers)
+  if (f32) return (const void *)linear_kernel<MODE, MODE == LN_PAIRS ? 128 : BT, false, true>;
+  return (const void *)linear_kernel<MODE, BT, false, false>;
 }
 
-qmoe_status ln_launch(const void *fn, int smem, const LnArgs &a, int grid, int cluster, cudaStream_t s) {
+qmoe_status ln_launch(const void *fn, int smem, int threads, const LnArgs &a, int grid, int cluster, cudaStream_t s) {
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QMOE_ERR_CUDA;
   LnArgs args = a;
   void *params[] = {&args};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(LN_THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -660,9 +769,21 @@ extern "C" qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, i
   g.split = 1;
   g.status = dev_status;
   const int sms = num_sms();
-  const bool vec = ldo * os % 16 == 0 && (!residual || ldr * os % 16 == 0);
-  const int mode = M <= 64 || !vec ? LN_FEATURES : M > 128 && N > 128 ? LN_PAIRS : LN_TOKENS;
-  const int BT = mode == LN_FEATURES ? (M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128) : mode == LN_PAIRS ? 256 : 128;
+  // a tensor store ends on 16 bytes: a row whose end does not would be overwritten past it
+  const bool vec = (long long)N * os % 16 == 0 && ldo * os % 16 == 0 && (!residual || ldr * os % 16 == 0);
+  const bool f32 = g.out_f32;
+  // tokens or pairs where they fill half the machine (and rows can be stored
+  // 16 bytes at a time); else narrow tiles of features, with K split
+  int mode = LN_FEATURES;
+  if (vec && M > 64) {
+    const long long alone = (long long)((M + 127) / 128) * ((N + 127) / 128);
+    const long long pairs = (long long)((M + 255) / 256) * ((N + 255) / 256);
+    if (pairs * 2 >= sms) mode = LN_PAIRS;
+    else if (alone * 2 >= sms) mode = LN_TOKENS;
+  }
+  int BT = mode == LN_PAIRS && (i8 || !f32) ? 256 : 128;
+  if (mode == LN_FEATURES)
+    for (BT = 16; BT < M && (BT < 64 || (!vec && BT < 128)); BT *= 2) {}
   const int rows_a = mode == LN_FEATURES ? N : M, rows_b = mode == LN_FEATURES ? M : N;
   const int tile_a = mode == LN_PAIRS ? 2 * LN_ROWS : LN_ROWS;
   g.tiles_a = (rows_a + tile_a - 1) / tile_a;
@@ -671,11 +792,14 @@ extern "C" qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, i
   if (nt > 0x1fffffffLL) return QMOE_ERR_UNSUPPORTED;
   if (mode == LN_FEATURES && BT <= 64)
     while (g.split < LN_MAX_SPLIT && nt * g.split * 2 <= sms && g.ksteps >= g.split * 4) g.split *= 2;
-  if (!ln_map(&g.tm_a, mode == LN_FEATURES ? w : a, i8, K, rows_a, mode == LN_FEATURES ? ldw : lda, LN_ROWS) ||
-      !ln_map(&g.tm_b, mode == LN_FEATURES ? a : w, i8, K, rows_b, mode == LN_FEATURES ? lda : ldw, ln_b_rows(mode, BT)))
+  if (!ln_map(&g.tm_a, mode == LN_FEATURES ? w : a, es, K, rows_a, mode == LN_FEATURES ? ldw : lda, LN_ROWS) ||
+      !ln_map(&g.tm_b, mode == LN_FEATURES ? a : w, es, K, rows_b, mode == LN_FEATURES ? lda : ldw, ln_b_rows(mode, BT)))
     return QMOE_ERR_CUDA;
+  if (mode != LN_FEATURES) {
+    if (!ln_map(&g.tm_out, out, os, N, M, ldo, 32)) return QMOE_ERR_CUDA;
+    if (residual && !ln_map(&g.tm_res, residual, os, N, M, ldr, 32)) return QMOE_ERR_CUDA;
+  }
   const void *fn;
-  const bool f32 = g.out_f32;
   if (mode == LN_FEATURES) {
     switch (BT) {
       case 16: fn = ln_kernel<LN_FEATURES, 16>(i8, f32); break;
@@ -686,9 +810,9 @@ extern "C" qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, i
   } else {
     fn = mode == LN_PAIRS ? ln_kernel<LN_PAIRS, 256>(i8, f32) : ln_kernel<LN_TOKENS, 128>(i8, f32);
   }
-  const int smem = ln_smem_bytes(mode, BT);
+  const int smem = ln_smem_bytes(mode, BT), threads = ln_threads(mode, BT);
   if ((size_t)smem > max_smem_optin()) return QMOE_ERR_UNSUPPORTED;
-  if (mode == LN_PAIRS) return ln_launch(fn, smem, g, 2 * (int)(nt < sms / 2 ? nt : sms / 2), 2, (cudaStream_t)stream);
-  const int grid = g.split > 1 ? (int)nt * g.split : (int)(nt < sms ? nt : sms);
-  return ln_launch(fn, smem, g, grid, g.split, (cudaStream_t)stream);
+  const int cluster = mode == LN_PAIRS ? 2 : g.split;
+  const int grid = cluster * (int)(nt < sms / cluster || g.split > 1 ? nt : sms / cluster);
+  return ln_launch(fn, smem, threads, g, grid, cluster, (cudaStream_t)stream);
 }

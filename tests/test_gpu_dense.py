@@ -239,9 +239,18 @@ def test_linear_strides(M, in_dtype):
         check_linear(make_linear(M, N, K, in_dtype, q.BF16, True, True, M, 192, 208, ldo, ldr), q.ACT_NONE)
 
 
+@pytest.mark.parametrize("M,N,K", [(700, 1700, 200), (1300, 1000, 72), (2100, 2600, 200), (4097, 1288, 136), (300, 9000, 64)])
+@pytest.mark.parametrize("in_dtype", [q.BF16, q.I8])
+def test_linear_large_tiles_with_ragged_ends(M, N, K, in_dtype):
+    """Tiles of 128 and pairs of 256 rows that end inside the matrix, padded rows, each output type."""
+    for n, (od, act, bias, res) in enumerate([(q.F32, q.ACT_SILU, True, True), (q.BF16, q.ACT_NONE, True, True),
+                                              (q.BF16, q.ACT_GELU, False, False), (q.F32, q.ACT_NONE, False, False)]):
+        check_linear(make_linear(M, N, K, in_dtype, od, bias, res, M + n, ldo=N + 8 * (n % 2) + (-N) % 8, ldr=N + 24 + (-N) % 8), act)
+
+
 def test_linear_residual_in_place_and_repeatable():
-    for M in (3, 40, 200):
-        d = make_linear(M, 256, 512, q.BF16, q.F32, False, True, M)
+    for M, N in ((3, 256), (40, 256), (200, 256), (700, 1704), (2100, 2600)):
+        d = make_linear(M, N, 512, q.BF16, q.F32, False, True, M)
         call_linear(d)
         first = d["out"][:M].clone()
         again = d["res"].clone()
