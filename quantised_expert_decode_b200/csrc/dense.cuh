@@ -137,6 +137,10 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// The same in two halves: arrive early, wait where the others' arrival matters.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // This CTA's shared object as it lies in CTA `rank` of the cluster (generic address).
 template <typename T>
 __device__ __forceinline__ T *peer(T *p, int rank) {

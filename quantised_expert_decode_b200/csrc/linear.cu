@@ -31,6 +31,8 @@
 // steps only, and the epilogue's threads add the slots' values with rounding.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "dense.cuh"
 #include "tc05.cuh"
 
@@ -80,16 +82,19 @@ __host__ __device__ constexpr int ln_epi_warps(int mode, int BT) { return mode =
 __host__ __device__ constexpr int ln_threads(int mode, int BT) { return 32 * (LN_W_EPI + ln_epi_warps(mode, BT)); }
 // Staging boxes: 16 in all, so one or two per warp.
 __host__ __device__ constexpr int ln_boxes(int mode) { return mode == LN_FEATURES ? 0 : 16; }
+// What the CTAs that split K send one another: a tile's accumulators.
+__host__ __device__ constexpr int ln_xch_bytes(int mode, int BT) { return mode == LN_FEATURES && BT <= 64 ? BT * LN_ROWS * 4 : 0; }
 // Rows of the B operand that one CTA loads.
 __host__ __device__ constexpr int ln_b_rows(int mode, int BT) { return mode == LN_PAIRS ? BT / 2 : BT; }
 __host__ __device__ constexpr int ln_stage_bytes(int mode, int BT) { return LN_A_BYTES + ln_b_rows(mode, BT) * LN_KB; }
 __host__ __device__ constexpr int ln_stages(int mode, int BT) {
-  return (LN_SMEM - ln_boxes(mode) * LN_BOX) / ln_stage_bytes(mode, BT) < LN_MAX_STAGES
-             ? (LN_SMEM - ln_boxes(mode) * LN_BOX) / ln_stage_bytes(mode, BT)
+  return (LN_SMEM - ln_boxes(mode) * LN_BOX - ln_xch_bytes(mode, BT)) / ln_stage_bytes(mode, BT) < LN_MAX_STAGES
+             ? (LN_SMEM - ln_boxes(mode) * LN_BOX - ln_xch_bytes(mode, BT)) / ln_stage_bytes(mode, BT)
              : LN_MAX_STAGES;
 }
 constexpr int ln_smem_bytes(int mode, int BT) {
-  return 1024 + ln_stages(mode, BT) * ln_stage_bytes(mode, BT) + ln_boxes(mode) * LN_BOX + (int)sizeof(LnBars);
+  return 1024 + ln_stages(mode, BT) * ln_stage_bytes(mode, BT) + ln_boxes(mode) * LN_BOX + ln_xch_bytes(mode, BT) +
+         (int)sizeof(LnBars);
 }
 // TMEM columns of the two accumulator slots: a power of two of at least 32
 __host__ __device__ constexpr int ln_tmem_cols(int BT) { return 2 * BT < 32 ? 32 : 2 * BT; }
@@ -157,11 +162,6 @@ __device__ __forceinline__ float ln_gelu(float v) {
 __device__ __forceinline__ float ln_relu(float v) { return v > 0.0f ? v : (v == v ? 0.0f : v); }
 __device__ __forceinline__ float ln_silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
-__device__ __forceinline__ float ln_act(float v, int act) {
-  if (act == QMOE_ACT_NONE) return v;
-  if (act == QMOE_ACT_RELU) return ln_relu(v);
-  return act == QMOE_ACT_SILU ? ln_silu(v) : ln_gelu(v);
-}
 template <int W>
 __device__ __forceinline__ void ln_act_all(float (&v)[W], int act) {
   if (act == QMOE_ACT_SILU) {
@@ -193,15 +193,6 @@ __device__ __forceinline__ float ln_load(const void *p, long long i, int f32) {
 __device__ __forceinline__ void ln_store(void *p, long long i, int f32, float v) {
   if (f32) static_cast<float *>(p)[i] = v;
   else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-}
-
-// One value of the result from its accumulator.
-template <bool I8>
-__device__ __forceinline__ void ln_finish(const LnArgs &a, float bits, int m, int n, float sw, float bias) {
-  float v = ln_acc<I8>(bits, I8 ? __ldg(a.s_a + m) : 1.0f, sw) + bias;
-  v = ln_act(v, a.act);
-  if (a.res) v += ln_load(a.res, (long long)m * a.ldr + n, a.out_f32);
-  ln_store(a.out, (long long)m * a.ldo + n, a.out_f32, v);
 }
 
 // Epilogue of a tile whose 128 rows are features: lane = feature, 16 columns = tokens.
@@ -298,7 +289,8 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
   constexpr int EPI_COLS = BT < 32 ? BT : BT / (N_EPI / 4);  // columns of an epilogue warp
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ln_smem) + 1023) & ~(uintptr_t)1023);
   uint8_t *boxes = sm + STAGES * STAGE;
-  LnBars *b = reinterpret_cast<LnBars *>(boxes + ln_boxes(MODE) * LN_BOX);
+  float *xch = reinterpret_cast<float *>(boxes + ln_boxes(MODE) * LN_BOX);
+  LnBars *b = reinterpret_cast<LnBars *>(reinterpret_cast<uint8_t *>(xch) + ln_xch_bytes(MODE, BT));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIRS || a.split > 1 ? (int)dense::cluster_rank() : 0;
   if (threadIdx.x == 0) {
@@ -330,6 +322,7 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
   tc05::fence_before_sync();
   __syncthreads();
   if (PAIRS) dense::cluster_sync();   // the other CTA's barriers are ready
+  else if (a.split > 1) dense::cluster_arrive();   // (waited for before the CTAs exchange sums)
   tc05::fence_after_sync();
   const uint32_t tmem = b->tmem_base;
   const int ntiles = a.tiles_a * a.tiles_b;
@@ -610,12 +603,11 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
     if (a.split > 1) {
       // one tile per cluster. The accumulators of feature f go to CTA
       // f / (128 / split), [source CTA][token][its features], through
-      // distributed shared memory over the finished ring.
-      const int fl = LN_ROWS / a.split;
+      // distributed shared memory.
+      const int fs = 7 - (31 - __clz(a.split)), fl = 1 << fs;   // features per CTA: 128 / split
       int ta, tb;
       ln_tile(a, first, ta, tb);
-      float *xch = reinterpret_cast<float *>(sm);
-      const int w = warp - LN_W_EPI, q = warp & 3, half = w >> 2, f = q * 32 + lane;
+      const int q = warp & 3, half = (warp - LN_W_EPI) >> 2, f = q * 32 + lane;
       const int col0 = BT < 32 ? 0 : half * EPI_COLS;
       constexpr int NCH = EPI_COLS / 16;
       float v[NCH][16];
@@ -640,31 +632,45 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
           if (lane == 0) mbar_arrive(&b->acc_empty[slot]);
         }
       }
-      __syncthreads();         // this CTA's products have read their ring (the MMA warp has waited for them)
-      dense::cluster_sync();   // and every other CTA's
+      dense::cluster_wait();   // every CTA of the cluster is running
       if (have && (BT >= 32 || half == 0)) {
-        float *dst = dense::peer(xch, f / fl) + rank * BT * fl + f % fl;
+        float *dst = dense::peer(xch, f >> fs) + ((rank * BT) << fs) + (f & (fl - 1));
+        const int mm = min(EPI_COLS, a.M - tb * BT - col0);
 #pragma unroll
         for (int h = 0; h < NCH; ++h)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) dst[(col0 + 16 * h + i) * fl] = v[h][i];
+          for (int i = 0; i < 16; ++i)
+            if (16 * h + i < mm) dst[(col0 + 16 * h + i) << fs] = v[h][i];
       }
       __syncwarp();
       dense::cluster_sync();
-      const int m0 = tb * BT, mn = min(BT, a.M - m0), n0 = ta * LN_ROWS + rank * fl;
-      for (int i = threadIdx.x; i < mn * fl; i += THREADS) {
-        const int m = i / fl, fi = i - m * fl, n = n0 + fi;
-        if (n >= a.N) continue;
-        float acc;
-        if (I8) {
-          int s = 0;
-          for (int r = 0; r < a.split; ++r) s += __float_as_int(xch[(r * BT + m) * fl + fi]);
-          acc = __int_as_float(s);
-        } else {
-          acc = 0.0f;
-          for (int r = 0; r < a.split; ++r) acc = __fadd_rn(acc, xch[(r * BT + m) * fl + fi]);
+      const int m0 = tb * BT, total = min(BT, a.M - m0) << fs, n0 = ta * LN_ROWS + (rank << fs);
+      // four values a thread at once: their loads in flight together
+      for (int i0 = threadIdx.x; i0 < total; i0 += 4 * THREADS) {
+        float x[4], res[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = min(i0 + j * THREADS, total - 1), m = i >> fs, n = min(n0 + (i & (fl - 1)), a.N - 1);
+          float acc = 0.0f;
+          int sum = 0;
+          for (int r = 0; r < a.split; ++r) {
+            const float y = xch[((r * BT + m) << fs) + (i & (fl - 1))];
+            if (I8) sum += __float_as_int(y);
+            else acc = __fadd_rn(acc, y);
+          }
+          x[j] = ln_acc<I8>(I8 ? __int_as_float(sum) : acc, I8 ? __ldg(a.s_a + m0 + m) : 1.0f, I8 ? __ldg(a.s_w + n) : 1.0f) +
+                 (a.bias ? __ldg(a.bias + n) : 0.0f);
+          res[j] = a.res ? ln_load(a.res, (long long)(m0 + m) * a.ldr + n, a.out_f32) : 0.0f;
         }
-        ln_finish<I8>(a, acc, m0 + m, n, I8 ? __ldg(a.s_w + n) : 1.0f, a.bias ? __ldg(a.bias + n) : 0.0f);
+        ln_act_all(x, a.act);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + j * THREADS, n = n0 + (i & (fl - 1));
+          if (i < total && n < a.N) {
+            const float y = a.res ? x[j] + res[j] : x[j];
+            ln_store(a.out, (long long)(m0 + (i >> fs)) * a.ldo + n, a.out_f32, y);
+          }
+        }
       }
     }
   }
@@ -704,6 +710,37 @@ const void *ln_kernel(bool i8, bool f32) {
   // (fp32 results from wide pairs: a thread's sums do not fit its registers)
   if (f32) return (const void *)linear_kernel<MODE, MODE == LN_PAIRS ? 128 : BT, false, true>;
   return (const void *)linear_kernel<MODE, BT, false, false>;
+}
+
+// Clusters of `size` CTAs, one CTA per SM, that run at once on this device (a
+// cluster lies within one part of the chip: 16 clusters of 8 do not fit on 148
+// SMs, and a second wave costs more than a narrower split).
+int ln_max_clusters(int size) {
+  static std::atomic<int> known[16][LN_MAX_SPLIT + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return 0;
+  int n = known[dev][size].load(std::memory_order_relaxed);
+  if (n == 0) {
+    const void *fn = (const void *)linear_kernel<LN_FEATURES, 16, true, false>;
+    const int smem = ln_smem_bytes(LN_FEATURES, 16);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(ln_threads(LN_FEATURES, 16));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev][size].store(n, std::memory_order_relaxed);
+  }
+  return n;
 }
 
 qmoe_status ln_launch(const void *fn, int smem, int threads, const LnArgs &a, int grid, int cluster, cudaStream_t s) {
@@ -782,16 +819,32 @@ extern "C" qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, i
     else if (alone * 2 >= sms) mode = LN_TOKENS;
   }
   int BT = mode == LN_PAIRS && (i8 || !f32) ? 256 : 128;
-  if (mode == LN_FEATURES)
-    for (BT = 16; BT < M && (BT < 64 || (!vec && BT < 128)); BT *= 2) {}
+  if (mode == LN_FEATURES && (vec || M <= 64)) {
+    // the tile width and split of K with the least time in cycles: a step takes
+    // 2.9 per operand row (measured: 45 bytes a cycle and SM), an exchange and
+    // the values' way out 3000 + 40 per token of the tile
+    double best = 0.0;
+    for (int bt = 16; bt <= 64; bt *= 2) {
+      const long long tiles = (long long)((N + LN_ROWS - 1) / LN_ROWS) * ((M + bt - 1) / bt);
+      int split = 1;
+      for (int s = 2; s <= LN_MAX_SPLIT && tiles * s <= sms && g.ksteps >= 2 * s; s *= 2)
+        if (tiles <= ln_max_clusters(s)) split = s;
+      const double waves = (double)((tiles * split + sms - 1) / sms);
+      const double t = waves * ((g.ksteps + split - 1) / split * 2.9 * (LN_ROWS + bt)) + 3000.0 + 40.0 * bt;
+      if (bt == 16 || t < best) {
+        best = t;
+        BT = bt;
+        g.split = split;
+      }
+      if (bt >= M) break;
+    }
+  }
   const int rows_a = mode == LN_FEATURES ? N : M, rows_b = mode == LN_FEATURES ? M : N;
   const int tile_a = mode == LN_PAIRS ? 2 * LN_ROWS : LN_ROWS;
   g.tiles_a = (rows_a + tile_a - 1) / tile_a;
   g.tiles_b = (rows_b + BT - 1) / BT;
   const long long nt = (long long)g.tiles_a * g.tiles_b;
   if (nt > 0x1fffffffLL) return QMOE_ERR_UNSUPPORTED;
-  if (mode == LN_FEATURES && BT <= 64)
-    while (g.split < LN_MAX_SPLIT && nt * g.split * 2 <= sms && g.ksteps >= g.split * 4) g.split *= 2;
   if (!ln_map(&g.tm_a, mode == LN_FEATURES ? w : a, es, K, rows_a, mode == LN_FEATURES ? ldw : lda, LN_ROWS) ||
       !ln_map(&g.tm_b, mode == LN_FEATURES ? a : w, es, K, rows_b, mode == LN_FEATURES ? lda : ldw, ln_b_rows(mode, BT)))
     return QMOE_ERR_CUDA;
