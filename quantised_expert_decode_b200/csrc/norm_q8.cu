@@ -4,17 +4,23 @@
 //   A = max |p| over the scale's columns (the row, or a group of 32/64/128)
 //   codes = rint(127 p / A) (ties to even),  scale = A r / 127
 // r cancels in the codes, so they follow from p alone, and they are formed
-// exactly: a code is taken from fp32 arithmetic (off by at most 3.1e-5 at
-// |127 p / A| <= 127: four roundings of 2^-24 relative) unless that value lies
-// within 1e-4 of a rounding border, where the thread repeats its columns with
-// the exact float64 products (two 24-bit factors) and a float64 division.
+// exactly: a code is taken from fp32 arithmetic (five roundings of 2^-24
+// relative) unless that lies within its error of a rounding border. Such a code
+// (8 in a million) is decided by two float64 products with A's fp32 value, and
+// where that value's own rounding leaves it open by the exact A, the largest
+// exact product (of two 24-bit factors).
 // r and the scales are fp32 values from an fp32 sum of squares; rows whose
 // fp32 sum or products leave the normal range are repeated in float64.
 //
-// Bound: HBM bandwidth (one read of x and y, one write per output; z stays in
-// registers between the statistics and the codes). One CTA per row at a time,
-// 8 columns per thread and load, CTAs loop over rows with the gain in
-// registers, and one CTA barrier per row carries both statistics.
+// Bound: HBM bandwidth for fp32 rows (one read of x and y, one write per output; z
+// waits in shared memory between the statistics and the codes: 8192 x 2048 with
+// x, y and z in fp32 41.6 us, 80 % of the measured copy rate), for bf16 rows the
+// issue of some 40 instructions a column (8192 x 2048 with the normed rows too 33.6 us,
+// 69 %). One CTA per row at a time, 8 neighbouring columns per thread and round, CTAs
+// loop over rows, two rows' z in turn, so that one CTA barrier per row carries all
+// statistics; the next row is fetched into L2 meanwhile. What is rare follows the
+// loop as loops of its own: called, or inlined where it is found, it took registers
+// from every row (a third of the speed).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -24,10 +30,9 @@ namespace {
 
 constexpr int NQ_VEC = 8;                    // columns per thread and chunk: 16 bytes of bf16, 8 bytes of codes
 constexpr int NQ_MAX_THREADS = 512;
-constexpr int NQ_MAX_CHUNKS = 4;
-constexpr int NQ_MAX_H = NQ_VEC * NQ_MAX_THREADS * NQ_MAX_CHUNKS;
+constexpr int NQ_MAX_H = 16384;
 constexpr float NQ_MAGIC = 12582912.0f;      // 1.5 * 2^23: adding it rounds to an integer, ties to even
-constexpr float NQ_NEAR = 0.4999f;           // fp32 codes this close to a border are settled in float64
+constexpr float NQ_ERR = 3.1e-7f;            // bound of a code's fp32 error relative to it: five roundings of 2^-24
 // fp32 statistics outside these are formed again in float64
 constexpr float NQ_LO = 1e-25f, NQ_HI = 1e25f;
 
@@ -74,15 +79,6 @@ __device__ __forceinline__ uint4 nq_bf16x8(const float (&v)[NQ_VEC]) {
 // finite value and NaNs above those.
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// A product's exact magnitude is its fp32 value plus this remainder (exact by
-// fused multiply-add for products well inside the fp32 range).
-__device__ __forceinline__ float remainder_of(float z, float g, float hi) { return __fmaf_rn(fabsf(z), fabsf(g), -hi); }
-
-__device__ __forceinline__ float lanes_max(float m, int width) {
-  for (int o = width >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
-}
-
 // Largest |p| in float64 over `width` adjacent lanes; magnitudes' bits order
 // like the magnitudes, NaN above everything.
 __device__ __forceinline__ double lanes_max_abs(double v, int width) {
@@ -94,290 +90,327 @@ __device__ __forceinline__ double lanes_max_abs(double v, int width) {
   return __longlong_as_double((long long)m);
 }
 
-template <int N>
-__device__ __forceinline__ double thread_max_abs(const float (&z)[N], const float *g) {
-  unsigned long long m = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const double p = g ? (double)z[i] * (double)g[i] : (double)z[i];
-    const unsigned long long n = (unsigned long long)__double_as_longlong(fabs(p));
-    m = n > m ? n : m;
-  }
-  return __longlong_as_double((long long)m);
-}
-
 __device__ __forceinline__ double wider(double a, double b) {
   return (unsigned long long)__double_as_longlong(a) > (unsigned long long)__double_as_longlong(b) ? a : b;
 }
 
 __device__ __forceinline__ bool in_range(float v) { return v >= NQ_LO && v <= NQ_HI; }
 
-// One code from the exact quotient.
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+struct NqShared {
+  float ss[2][NQ_MAX_THREADS / 32];
+  uint32_t hi[2][NQ_MAX_THREADS / 32];
+  double d[NQ_MAX_THREADS / 32];
+};
+
+__device__ __forceinline__ void nq_get(const float *zs, int ch, float (&z)[NQ_VEC]) {
+  nq_load<false>(zs, (size_t)ch * NQ_VEC, z);
+}
+
+// ---- what is rare
+
+__device__ __forceinline__ float nq_gain1(const NqArgs &a, int h) { return a.gain ? __ldg(a.gain + h) : 1.0f; }
+
+// The float64 quotient's code.
 __device__ __forceinline__ int code_exact(double p, double A) { return (int)rint(__ddiv_rn(__dmul_rn(p, 127.0), A)); }
 
-template <bool BF16, int C, bool NORM>
-__global__ void __launch_bounds__(NQ_MAX_THREADS) norm_q8_kernel(NqArgs a) {
-  __shared__ float s_ss[2][NQ_MAX_THREADS / 32];
-  __shared__ uint32_t s_hi[2][NQ_MAX_THREADS / 32];
-  __shared__ float s_lo[2][NQ_MAX_THREADS / 32];
-  __shared__ double s_d[NQ_MAX_THREADS / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-  const int nchunk = a.H / NQ_VEC;
-  const bool has_gain = NORM && a.gain;
+// Largest |p| in float64 of the columns h0 .. h1 - 1, step by step (one thread).
+__device__ __forceinline__ double cols_max_abs(const NqArgs &a, const float *zs, int h0, int h1, int step) {
+  double m = 0.0;
+#pragma unroll 1
+  for (int h = h0; h < h1; h += step) m = wider(m, fabs((double)zs[h] * (double)nq_gain1(a, h)));
+  return m;
+}
 
-  float g[C][NQ_VEC];
-  if (NORM) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int ch = c * blockDim.x + tid;
-#pragma unroll
-      for (int i = 0; i < NQ_VEC; ++i) g[c][i] = 1.0f;
-      if (has_gain && ch < nchunk) nq_load<false>(a.gain, (size_t)ch * NQ_VEC, g[c]);
-    }
+// The codes near a border of one warp's chunks, from z's exact products with the
+// gain. A code between k and k + 1 is k + 1 where 254 |p| > (2 k + 1) A, two
+// float64 products; where A's fp32 value (known to 2^-24; exact without a gain)
+// does not decide it the exact A does: its fp32 value plus the largest remainder
+// among the products that round to it; and what that leaves open the quotient.
+// (The scan for that remainder takes 4 columns a lane with 4 loads in flight: in
+// single columns it took as long as several rows, 42 us for the 8192 x 2048 case.)
+__device__ __forceinline__ void settle(const NqArgs &a, const float *zs, int t, int ch, float Af, bool near) {
+  const int h0 = ch * NQ_VEC, lane = threadIdx.x & 31;
+  if (a.group != 0) {   // the group's largest |p| in fp32
+    uint32_t m = 0;
+#pragma unroll 1
+    for (int h = h0; h < min(h0 + NQ_VEC, a.H); ++h) m = max(m, mag(__fmul_rn(zs[h], nq_gain1(a, h))));
+    __syncwarp();
+    for (int o = a.group / NQ_VEC >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    Af = __uint_as_float(m);
   }
+  const float r = __fmul_rn(127.0f, __frcp_rn(Af));
+  double A = (double)Af;
+  bool exact = !a.gain;
+  unsigned ties = 0;
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    bool open = false;
+    if (near) {
+      float z[NQ_VEC], g[NQ_VEC];
+      nq_get(zs, ch, z);
+#pragma unroll
+      for (int i = 0; i < NQ_VEC; ++i) g[i] = 1.0f;
+      if (a.gain) nq_load<false>(a.gain, h0, g);
+#pragma unroll
+      for (int i = 0; i < NQ_VEC; ++i) {
+        const float v = __fmul_rn(__fmul_rn(z[i], g[i]), r);
+        if (__fmaf_rn(fabsf(v), NQ_ERR, fabsf(v - rintf(v))) <= 0.499999f) continue;
+        const double p = (double)z[i] * (double)g[i];
+        const float f = floorf(fabsf(v));
+        const double left = 254.0 * fabs(p), right = (double)(2.0f * f + 1.0f) * A;
+        int k = (int)f + (left > right ? 1 : 0);
+        k = v < 0.0f ? -k : k;
+        bool tie = false;
+        if (fabs(left - right) <= (exact ? 1e-14 : 1.3e-7) * right) {
+          tie = exact;
+          open |= !exact;
+        }
+        if (tie) ties |= 1u << i;
+        a.codes[(size_t)t * a.H + h0 + i] = (int8_t)k;
+      }
+#pragma unroll 1
+      for (; ties; ties &= ties - 1) {
+        const int h = h0 + __ffs(ties) - 1;
+        a.codes[(size_t)t * a.H + h] = (int8_t)code_exact((double)zs[h] * (double)nq_gain1(a, h), A);
+      }
+    }
+    if (exact || !__any_sync(0xffffffffu, open)) break;
+    float lo = -INFINITY;
+    const int c0 = a.group ? h0 : 4 * lane, c1 = a.group ? min(h0 + NQ_VEC, a.H) : a.H, cs = a.group ? 4 : 128;
+#pragma unroll 4
+    for (int h = c0; h < c1; h += cs) {
+      const float4 z = *reinterpret_cast<const float4 *>(zs + h), g = __ldg(reinterpret_cast<const float4 *>(a.gain + h));
+      const float zz[4] = {z.x, z.y, z.z, z.w}, gg[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float rem = __fmaf_rn(fabsf(zz[i]), fabsf(gg[i]), -Af);
+        lo = fmaxf(lo, mag(__fmul_rn(zz[i], gg[i])) == mag(Af) ? rem : -INFINITY);
+      }
+    }
+    __syncwarp();
+    for (int o = (a.group ? a.group / NQ_VEC : 32) >> 1; o > 0; o >>= 1) lo = fmaxf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    A = (double)Af + (double)lo;
+    exact = true;
+  }
+}
+
+// A chunk of one warp in float64: the row's A (or its own groups'), 1 / rms.
+__device__ __forceinline__ void chunk_slow(const NqArgs &a, const float *zs, int t, int ch, double A, double r) {
+  const int gl = a.group / NQ_VEC, h0 = ch * NQ_VEC, h1 = min(h0 + NQ_VEC, a.H);
+  if (a.group != 0) A = lanes_max_abs(cols_max_abs(a, zs, h0, h1, 1), gl);
+  const bool finite = A <= 1.7e308 && r == r;   // neither NaN nor infinite
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    const double p = (double)zs[h] * (double)nq_gain1(a, h);
+    if (a.norm) a.norm[(size_t)t * a.H + h] = __float2bfloat16_rn(__double2float_rn(p * r));
+    if (a.codes) a.codes[(size_t)t * a.H + h] = (int8_t)(finite && A > 0.0 ? code_exact(p, A) : 0);
+  }
+  if (!a.codes || h0 >= a.H) return;
+  const float sc = finite ? __double2float_rn(A * r / 127.0) : __uint_as_float(0x7fffffffu);
+  if (a.group == 0) {
+    if (ch == 0) a.scales[t] = sc;
+  } else if ((ch & (gl - 1)) == 0) {
+    a.scales[((size_t)t * a.H + h0) / a.group] = sc;
+  }
+}
+
+// 1 / rms of a row in float64 (whole CTA). A NaN or an infinity makes it NaN.
+__device__ __forceinline__ double row_inverse(const NqArgs &a, const float *zs, NqShared *sh) {
+  double d = 0.0;
+  // (each thread its own columns: the others' may not be there yet)
+  for (int ch = threadIdx.x; ch < a.H / NQ_VEC; ch += blockDim.x)
+#pragma unroll 1
+    for (int i = 0; i < NQ_VEC; ++i) d = fma((double)zs[ch * NQ_VEC + i], (double)zs[ch * NQ_VEC + i], d);
+  d = warp_sum_d(d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh->d[threadIdx.x >> 5] = d;
+  __syncthreads();
+  d = 0.0;
+  for (int w = 0; w < (int)blockDim.x >> 5; ++w) d += sh->d[w];
+  const double m = d / a.H + (double)a.eps;
+  return d <= 1.7e308 ? (m > 0.0 ? 1.0 / sqrt(m) : 0.0) : __longlong_as_double(0x7ff8000000000000ll);
+}
+
+template <bool BF16, bool NORM>
+__global__ void __launch_bounds__(NQ_MAX_THREADS, 2) norm_q8_kernel(const __grid_constant__ NqArgs a) {
+  extern __shared__ __align__(16) float z_rows[];   // two rows' z, in turn
+  __shared__ NqShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  const int nchunk = a.H / NQ_VEC, step = blockDim.x;
+  const bool row_scale = a.group == 0 && a.codes, gain = NORM && a.gain;
+  const int gl = a.group / NQ_VEC;   // lanes per group
+  const float inv_h = 1.0f / (float)a.H;
 
   int par = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
     const size_t row = (size_t)t * a.H;
-    float z[C][NQ_VEC];
+    float *zs = z_rows + par * a.H;
     float ss = 0.0f;
-    uint32_t hi = 0;      // this thread's largest |p| in fp32 (all chunks; used for a row scale)
-    uint32_t hic[C];      // per chunk (used for group scales)
+    uint32_t hi = 0;   // magnitude bits of this thread's largest |p| in fp32
+#pragma unroll 2
+    for (int ch = tid; ch < nchunk; ch += step) {
+      const size_t e = row + (size_t)ch * NQ_VEC;
+      float z[NQ_VEC];
+      nq_load<BF16>(a.x, e, z);
+      if (NORM && a.y) {
+        float y[NQ_VEC];
+        nq_load<BF16>(a.y, e, y);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int ch = c * blockDim.x + tid;
-      if (ch < nchunk) nq_load<BF16>(a.x, row + (size_t)ch * NQ_VEC, z[c]);
-      else
-#pragma unroll
-        for (int i = 0; i < NQ_VEC; ++i) z[c][i] = 0.0f;
-    }
-    if (NORM && a.y) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int ch = c * blockDim.x + tid;
-        if (ch < nchunk) {
-          float yv[NQ_VEC];
-          nq_load<BF16>(a.y, row + (size_t)ch * NQ_VEC, yv);
-#pragma unroll
-          for (int i = 0; i < NQ_VEC; ++i) z[c][i] = __fadd_rn(z[c][i], yv[i]);
+        for (int i = 0; i < NQ_VEC; ++i) z[i] = __fadd_rn(z[i], y[i]);
+      }
+      float4 *q = reinterpret_cast<float4 *>(zs + ch * NQ_VEC);
+      q[0] = make_float4(z[0], z[1], z[2], z[3]);
+      q[1] = make_float4(z[4], z[5], z[6], z[7]);
+      if (NORM && a.z) {   // the updated residual stream
+        if (BF16) {
+          *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.z) + e) = nq_bf16x8(z);
+        } else {
+          float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.z) + e);
+          o[0] = make_float4(z[0], z[1], z[2], z[3]);
+          o[1] = make_float4(z[4], z[5], z[6], z[7]);
         }
       }
-    }
+      if (NORM)
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      hic[c] = 0;
+        for (int i = 0; i < NQ_VEC; ++i) ss = __fmaf_rn(z[i], z[i], ss);
+      if (row_scale) {
+        if (gain) {
+          float g[NQ_VEC];
+          nq_load<false>(a.gain, (size_t)ch * NQ_VEC, g);
 #pragma unroll
-      for (int i = 0; i < NQ_VEC; ++i) {
-        if (NORM) ss = __fmaf_rn(z[c][i], z[c][i], ss);
-        hic[c] = max(hic[c], mag(NORM ? __fmul_rn(z[c][i], g[c][i]) : z[c][i]));
-      }
-      hi = max(hi, hic[c]);
-    }
-    // the updated residual stream leaves as early as it can
-    if (NORM && a.z) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int ch = c * blockDim.x + tid;
-        if (ch < nchunk) {
-          if (BF16) {
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.z) + row + (size_t)ch * NQ_VEC) = nq_bf16x8(z[c]);
-          } else {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.z) + row + (size_t)ch * NQ_VEC);
-            o[0] = make_float4(z[c][0], z[c][1], z[c][2], z[c][3]);
-            o[1] = make_float4(z[c][4], z[c][5], z[c][6], z[c][7]);
-          }
+          for (int i = 0; i < NQ_VEC; ++i) z[i] = __fmul_rn(z[i], g[i]);
         }
+#pragma unroll
+        for (int i = 0; i < NQ_VEC; ++i) hi = max(hi, mag(z[i]));
       }
     }
 
-    // row statistics: the sum of squares, and for a row scale the exact
-    // largest |p|: the largest remainder among the products whose fp32 value
-    // is the warp's largest, then among the warps that hold the row's largest
-    float inv = 1.0f;
-    double invd = 1.0;    // the same in float64 where `wide`
-    bool wide = false;
-    const bool row_scale = a.group == 0 && a.codes;
-    const uint32_t whi = __reduce_max_sync(0xffffffffu, hi);
-    if (row_scale) {
-      float lo = -INFINITY;
-      if (hi == whi) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < NQ_VEC; ++i) {
-            const float gv = NORM ? g[c][i] : 1.0f;
-            if (mag(__fmul_rn(z[c][i], gv)) == whi) lo = fmaxf(lo, remainder_of(z[c][i], gv, __uint_as_float(whi)));
-          }
+    // the CTA's next row on its way into L2 while this one is worked on
+    if (t + (int)gridDim.x < a.T && (lane & (BF16 ? 7 : 3)) == 0)   // (a 128-byte line per 8 or 4 lanes)
+      for (int ch = tid; ch < nchunk; ch += step) {
+        const size_t e = row + (size_t)gridDim.x * a.H + (size_t)ch * NQ_VEC;
+        prefetch_l2(static_cast<const uint8_t *>(a.x) + e * (BF16 ? 2 : 4));
+        if (NORM && a.y) prefetch_l2(static_cast<const uint8_t *>(a.y) + e * (BF16 ? 2 : 4));
       }
-      lo = lanes_max(lo, 32);
-      if (lane == 0) s_lo[par][warp] = lo;
-    }
+
+    // row statistics
     if (NORM) {
       ss = warp_sum(ss);
-      if (lane == 0) s_ss[par][warp] = ss;
+      if (lane == 0) sh.ss[par][warp] = ss;
     }
-    if (lane == 0) s_hi[par][warp] = whi;
+    if (row_scale) {
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) sh.hi[par][warp] = hi;
+    }
     __syncthreads();
     uint32_t rhi = 0;
-    float rss = 0.0f, rlo = -INFINITY;
+    float rss = 0.0f;
     for (int w = 0; w < nw; ++w) {
-      rhi = max(rhi, s_hi[par][w]);
-      if (NORM) rss += s_ss[par][w];
+      if (NORM) rss += sh.ss[par][w];
+      rhi = max(rhi, sh.hi[par][w]);
     }
-    double Arow = 0.0;
-    if (row_scale) {
-      for (int w = 0; w < nw; ++w)
-        if (s_hi[par][w] == rhi) rlo = fmaxf(rlo, s_lo[par][w]);
-      Arow = (double)__uint_as_float(rhi) + (double)rlo;
-      if (!in_range(__uint_as_float(rhi))) {   // uniform over the CTA: fp32 products cannot be trusted
-        double m = 0.0;
-#pragma unroll
-        for (int c = 0; c < C; ++c) m = wider(m, thread_max_abs(z[c], NORM ? g[c] : nullptr));
-        m = lanes_max_abs(m, 32);
-        __syncthreads();
-        if (lane == 0) s_d[warp] = m;
-        __syncthreads();
-        Arow = 0.0;
-        for (int w = 0; w < nw; ++w) Arow = wider(Arow, s_d[w]);
-      }
-    }
-    if (NORM) {
-      if (in_range(rss)) {
-        inv = rsqrtf(__fdiv_rn(rss, (float)a.H) + a.eps);
-      } else {   // tiny, huge or non-finite rows: the sum of squares and r in float64
-        wide = true;
-        double d = 0.0;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < NQ_VEC; ++i) d = fma((double)z[c][i], (double)z[c][i], d);
-        d = warp_sum_d(d);
-        __syncthreads();
-        if (lane == 0) s_d[warp] = d;
-        __syncthreads();
-        d = 0.0;
-        for (int w = 0; w < nw; ++w) d += s_d[w];
-        // a NaN or an infinity in the row makes every value of it NaN
-        const double m = d / a.H + (double)a.eps;
-        invd = d <= 1.7e308 ? (m > 0.0 ? 1.0 / sqrt(m) : 0.0) : __longlong_as_double(0x7ff8000000000000ll);
-        inv = __double2float_rn(invd);
-      }
-    }
-    if (NORM && a.norm) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int ch = c * blockDim.x + tid;
-        if (ch < nchunk) {
-          float v[NQ_VEC];
-#pragma unroll
-          for (int i = 0; i < NQ_VEC; ++i) v[i] = __fmul_rn(__fmul_rn(z[c][i], inv), g[c][i]);
-          if (wide)
-#pragma unroll
-            for (int i = 0; i < NQ_VEC; ++i) v[i] = __double2float_rn((double)z[c][i] * (double)g[c][i] * invd);
-          *reinterpret_cast<uint4 *>(a.norm + row + (size_t)ch * NQ_VEC) = nq_bf16x8(v);
-        }
-      }
-    }
-    if (!a.codes) continue;
+    float Af = __uint_as_float(rhi), r = __fmul_rn(127.0f, __frcp_rn(Af));   // the scale's largest |p| in fp32
+    // (uniform) rows whose fp32 sum of squares or largest product leaves the normal
+    // range - tiny, huge, not finite - are done again below
+    const bool odd = (NORM && !in_range(rss)) || (row_scale && !in_range(Af));
+    const float inv = NORM ? rsqrtf(__fmaf_rn(rss, inv_h, a.eps)) : 1.0f;
 
-    const int gl = a.group / NQ_VEC;   // lanes per group
+    unsigned near = 0, slow = 0, bit = 1;   // rounds whose chunks are not settled yet
+#pragma unroll 1
+    for (int ch = tid; ch - lane < nchunk; ch += step, bit <<= 1) {   // (whole warps)
+      const bool live = ch < nchunk;
+      const size_t e = row + (size_t)ch * NQ_VEC;
+      float p[NQ_VEC];
+      nq_get(zs, live ? ch : 0, p);
+      if (gain) {
+        float g[NQ_VEC];
+        nq_load<false>(a.gain, (size_t)(live ? ch : 0) * NQ_VEC, g);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int ch = c * blockDim.x + tid;
-      if (c * blockDim.x + (tid & ~31) >= nchunk) break;   // the whole warp is past the row
-      double Ad = Arow;   // the scale's exact largest |p|
+        for (int i = 0; i < NQ_VEC; ++i) p[i] = __fmul_rn(p[i], g[i]);
+      }
+      if (NORM && a.norm) {
+        float v[NQ_VEC];
+#pragma unroll
+        for (int i = 0; i < NQ_VEC; ++i) v[i] = __fmul_rn(p[i], inv);
+        const uint4 o = nq_bf16x8(v);
+        if (live) *reinterpret_cast<uint4 *>(a.norm + e) = o;
+      }
+      if (!a.codes) continue;
+
       if (a.group != 0) {
-        uint32_t m = hic[c];
-        for (int o = gl >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float lo = -INFINITY;
-        if (hic[c] == m) {
+        uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < NQ_VEC; ++i) {
-            const float gv = NORM ? g[c][i] : 1.0f;
-            if (mag(__fmul_rn(z[c][i], gv)) == m) lo = fmaxf(lo, remainder_of(z[c][i], gv, __uint_as_float(m)));
-          }
-        }
-        lo = lanes_max(lo, gl);
-        Ad = (double)__uint_as_float(m) + (double)lo;
-        const bool odd = !in_range(__uint_as_float(m));
-        if (__any_sync(0xffffffffu, odd)) {
-          const double e = lanes_max_abs(thread_max_abs(z[c], NORM ? g[c] : nullptr), gl);
-          if (odd) Ad = e;
-        }
+        for (int i = 0; i < NQ_VEC; ++i) m = max(m, mag(p[i]));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));   // (at least 4 lanes)
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (gl > 4) m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        if (gl > 8) m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        Af = __uint_as_float(m);
+        r = __fmul_rn(127.0f, __frcp_rn(Af));
+        slow |= live && !in_range(Af) ? bit : 0u;
       }
-      const float A = __double2float_rn(Ad);
-      const bool plain = in_range(A) && !wide;
-      const bool finite = Ad <= 1.7e308 && inv == inv;   // neither NaN nor infinite
-      uint32_t lo4 = 0, hi4 = 0;
-      if (plain && finite) {
-        const float r = __fdiv_rn(127.0f, A);
-        float far = 0.0f;
+      uint2 codes;
+      float far = 0.0f;
+      {
+        uint32_t m[NQ_VEC];
 #pragma unroll
         for (int i = 0; i < NQ_VEC; ++i) {
-          const float v = __fmul_rn(NORM ? __fmul_rn(z[c][i], g[c][i]) : z[c][i], r);
-          const float m = __fadd_rn(v, NQ_MAGIC);
-          far = fmaxf(far, fabsf(__fsub_rn(v, __fsub_rn(m, NQ_MAGIC))));
-          const uint32_t b = __float_as_uint(m) & 0xffu;
-          if (i < 4) lo4 |= b << (8 * i);
-          else hi4 |= b << (8 * (i - 4));
+          const float v = __fmul_rn(p[i], r), q = __fadd_rn(v, NQ_MAGIC);
+          far = fmaxf(far, __fmaf_rn(fabsf(v), NQ_ERR, fabsf(__fsub_rn(v, __fsub_rn(q, NQ_MAGIC)))));
+          m[i] = __float_as_uint(q);
         }
-        if (far > NQ_NEAR) {
-          lo4 = hi4 = 0;
-#pragma unroll
-          for (int i = 0; i < NQ_VEC; ++i) {
-            const float gv = NORM ? g[c][i] : 1.0f;
-            const uint32_t b = (uint32_t)code_exact((double)z[c][i] * (double)gv, Ad) & 0xffu;
-            if (i < 4) lo4 |= b << (8 * i);
-            else hi4 |= b << (8 * (i - 4));
-          }
-        }
-      } else if (finite && Ad > 0.0) {
-#pragma unroll
-        for (int i = 0; i < NQ_VEC; ++i) {
-          const float gv = NORM ? g[c][i] : 1.0f;
-          const uint32_t b = (uint32_t)code_exact((double)z[c][i] * (double)gv, Ad) & 0xffu;
-          if (i < 4) lo4 |= b << (8 * i);
-          else hi4 |= b << (8 * (i - 4));
-        }
+        codes.x = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
+        codes.y = __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410);
       }
-      if (ch < nchunk) {
-        *reinterpret_cast<uint2 *>(a.codes + row + (size_t)ch * NQ_VEC) = make_uint2(lo4, hi4);
-        float sc;
-        if (!finite) sc = __uint_as_float(0x7fffffffu);
-        else if (plain) sc = __fdiv_rn(__fmul_rn(A, inv), 127.0f);
-        else sc = __double2float_rn(Ad * (wide ? invd : (double)inv) / 127.0);
+      near |= live && far > 0.499999f ? bit : 0u;
+      const float sc = __fmul_rn(__fmul_rn(Af, inv), 1.0f / 127.0f);
+      if (live) {
+        *reinterpret_cast<uint2 *>(a.codes + e) = codes;
         if (a.group == 0) {
           if (ch == 0) a.scales[t] = sc;
-        } else if (ch % gl == 0) {
-          a.scales[(size_t)t * (a.H / a.group) + ch / gl] = sc;
+        } else if ((ch & (gl - 1)) == 0) {
+          a.scales[((size_t)t * nchunk + ch) / gl] = sc;
         }
       }
     }
-  }
-}
-
-template <bool BF16, bool NORM>
-const void *nq_kernel(int C) {
-  switch (C) {
-    case 1: return (const void *)norm_q8_kernel<BF16, 1, NORM>;
-    case 2: return (const void *)norm_q8_kernel<BF16, 2, NORM>;
-    default: return (const void *)norm_q8_kernel<BF16, 4, NORM>;
+    // now and then: what the fp32 arithmetic left open, or could not do
+    const unsigned all = odd ? bit - 1u : 0u;   // (a warp's rounds so far)
+    unsigned m = __reduce_or_sync(0xffffffffu, near | slow | all);
+    if (m == 0) continue;
+    double A = 0.0, rd = (double)inv;
+    if (odd) {
+      if (NORM) rd = row_inverse(a, zs, &sh);
+      if (row_scale) A = lanes_max_abs(cols_max_abs(a, zs, lane, a.H, 32), 32);
+    }
+    for (; m; m &= m - 1) {
+      const int k = __ffs(m) - 1, ch = tid + k * step;
+      if (odd || __any_sync(0xffffffffu, slow >> k & 1)) chunk_slow(a, zs, t, ch, A, rd);
+      else settle(a, zs, t, ch, Af, near >> k & 1);
+    }
   }
 }
 
 qmoe_status nq_launch(const NqArgs &a, int dtype, bool norm, cudaStream_t s) {
-  const int nchunk = a.H / NQ_VEC;
-  int C = 1;
-  while (C < NQ_MAX_CHUNKS && nchunk > C * 256) C *= 2;
-  const int threads = ((nchunk + C - 1) / C + 31) / 32 * 32;
-  const void *fn = norm ? (dtype == QMOE_BF16 ? nq_kernel<true, true>(C) : nq_kernel<false, true>(C))
-                        : (dtype == QMOE_BF16 ? nq_kernel<true, false>(C) : nq_kernel<false, false>(C));
-  const int per_sm = 2048 / threads < 16 ? 2048 / threads : 16;
-  const long long cap = (long long)num_sms() * per_sm;
+  // many rows: 128 threads each, so that a thread's part of the reductions is shared
+  // by more columns; fewer than the SMs hold at once: more, for the shorter chain
+  // (1003 x 5248: 20.5 us with 256, 29.4 with 128, 23.2 with 512; 8192 x 2048: 33.8 with
+  // 128, 38.5 with 256; one row 2.8 with 512, 3.3 with 128)
+  const int nchunk = a.H / NQ_VEC, sms = num_sms();
+  const int most = a.T > 16 * sms ? 128 : a.T > 4 * sms ? 256 : NQ_MAX_THREADS;
+  const int threads = nchunk >= most ? most : (nchunk + 31) / 32 * 32;
+  const void *fn = norm ? (dtype == QMOE_BF16 ? (const void *)norm_q8_kernel<true, true> : (const void *)norm_q8_kernel<false, true>)
+                        : (dtype == QMOE_BF16 ? (const void *)norm_q8_kernel<true, false> : (const void *)norm_q8_kernel<false, false>);
+  const size_t smem = 2 * (size_t)a.H * sizeof(float);
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return QMOE_ERR_CUDA;
+  const long long cap = 1024LL / threads * sms;
   const int grid = a.T < cap ? a.T : (int)cap;
   NqArgs args = a;
   void *params[] = {&args};
-  const cudaError_t e = cudaLaunchKernel(fn, dim3(grid), dim3(threads), params, 0, s);
+  const cudaError_t e = cudaLaunchKernel(fn, dim3(grid), dim3(threads), params, smem, s);
   note_launch();
   return cuda_status(e);
 }
