@@ -119,7 +119,8 @@ def _p(t) -> int | None:
 def _s(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # (a Stream object takes 3 us to make)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -216,6 +217,11 @@ def _fits(fn: str, *wants) -> None:
     for t, dtype, rows, cols, ld in wants:
         if t is None or isinstance(t, int):
             continue
+        # a packed tensor of its own rows, as most are, with few questions to it; the others one by one
+        if t.dtype is getattr(torch, dtype) and t.get_device() == dev and t.is_contiguous():
+            shape = t.shape
+            if (ld == cols or not ld) and t.numel() >= rows * cols and (len(shape) < 2 or not ld or shape[-1] == ld):
+                continue
         if t.dtype != getattr(torch, dtype):
             raise QmoeError(fn + f" (a {t.dtype} tensor in the place of a {dtype} one)", 1)
         if t.get_device() != dev:
