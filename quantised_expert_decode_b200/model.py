@@ -104,3 +104,63 @@ class DecodeStack:
             self.close()
         except Exception:
             pass
+
+
+class TokenHead:
+    """What follows a layer stack: final RMSNorm -> vocabulary product -> sampled tokens, three kernels.
+
+    ``weight`` bf16 or fp32 [V, H]. With ``bits`` 8 its rows are kept as int8 codes and fp32 scales
+    (qmoe_quantise_rows) and the normed rows are 8-bit too; with ``bits`` 16 both are bf16. ``gain`` fp32 [H]
+    or None; ``bias`` fp32 [V] or None. All buffers are made here; ``step`` only launches, and can be captured.
+    Two steps that overlap on different streams need a head each.
+    """
+
+    def __init__(self, weight, T: int, gain=None, bias=None, eps: float = 1e-6, bits: int = 8, stream=None):
+        if weight.dim() != 2 or weight.dtype not in (torch.bfloat16, torch.float32):
+            raise L.QmoeError("TokenHead (weight must be a bf16 or fp32 matrix)", 1)
+        if bits not in (8, 16):
+            raise L.QmoeError("TokenHead (bits must be 8 or 16)", 1)
+        if T < 1:
+            raise L.QmoeError("TokenHead (no tokens)", 1)
+        self.V, self.H = weight.shape
+        self.T, self.eps, self.bits, self.gain, self.bias = T, eps, bits, gain, bias
+        dev = weight.device
+        if bits == 8:
+            self.weight = torch.empty((self.V, self.H), dtype=torch.int8, device=dev)
+            self.weight_scale = torch.empty(self.V, dtype=torch.float32, device=dev)
+            L.qmoe_quantise_rows(weight, L.BF16 if weight.dtype == torch.bfloat16 else L.F32, self.V, self.H, 0,
+                                 self.weight, self.weight_scale, stream)
+            self.codes = torch.empty((T, self.H), dtype=torch.int8, device=dev)
+            self.scale = torch.empty(T, dtype=torch.float32, device=dev)
+            self.norm = None
+        else:
+            self.weight, self.weight_scale = weight.to(torch.bfloat16).contiguous(), None
+            self.norm = torch.empty((T, self.H), dtype=torch.bfloat16, device=dev)
+            self.codes = self.scale = None
+        # rows of logits start on 16 bytes whatever V is
+        self._ld = (self.V + 3) // 4 * 4
+        self._logits = torch.empty((T, self._ld), dtype=torch.float32, device=dev)
+        self.logits = self._logits[:, :self.V]
+        self.token = torch.empty(T, dtype=torch.int32, device=dev)
+        self.prob = torch.empty(T, dtype=torch.float32, device=dev)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def step(self, x, u, temperature=None, top_k=None, top_p=None, min_p=None, y=None, stream=None) -> torch.Tensor:
+        """``x`` (and ``y``, added to it) fp32 or bf16 [T, H], for instance ``DecodeStack.x_out``; ``u`` fp32 [T] in
+        [0, 1), one per row; the rest as in qmoe_sample. Returns the device tensor ``token`` int32 [T]."""
+        if x.dtype not in (torch.bfloat16, torch.float32):
+            raise L.QmoeError("TokenHead.step (x must be bf16 or fp32)", 1)
+        if x.numel() != self.T * self.H:
+            raise L.QmoeError("TokenHead.step (x is not [T, H])", 1)
+        L.qmoe_rmsnorm_residual_q8(x, y, L.BF16 if x.dtype == torch.bfloat16 else L.F32, self.gain, self.eps, self.T,
+                                   self.H, 0, None, self.norm, self.codes, self.scale, stream)
+        a = self.codes if self.bits == 8 else self.norm
+        L.qmoe_linear(a, L.I8 if self.bits == 8 else L.BF16, self.weight, self.T, self.V, self.H, self.scale,
+                      self.weight_scale, self.bias, L.ACT_NONE, None, self._logits, L.F32, self.dev_status,
+                      ldo=self._ld, stream=stream)
+        L.qmoe_sample(self._logits, L.F32, self.T, self.V, temperature, top_k, top_p, min_p, u, self.token, self.prob,
+                      self.dev_status, ld=self._ld, stream=stream)
+        return self.token
+
+    def status(self) -> int:
+        return L.qmoe_read_status(self.dev_status)

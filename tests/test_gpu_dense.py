@@ -19,6 +19,9 @@ import torch
 
 import quantised_expert_decode_b200 as q
 from oracle import dense
+from quantised_expert_decode_b200.model import DecodeStack, TokenHead
+from synth import configs, gen
+from synth.workload import device_layers
 from tests.gpu_util import status_word, to_np
 
 pytestmark = pytest.mark.gpu
@@ -120,6 +123,28 @@ def test_norm_extreme_rows(group):
     _, _, codes, scales = run_norm(dev(x[8:]), None, q.F32, dev(gain), group)
     _, _, co, so = dense.norm_q8(x[8:], None, gain, 1e-6, group)
     assert np.array_equal(to_np(codes), co) and np.array_equal(np.isnan(to_np(scales)), np.isnan(so))
+
+
+@pytest.mark.parametrize("T,H,group", [(2500, 272, 0), (2500, 1056, 32), (700, 4112, 0), (700, 5248, 64), (149, 2048, 128)])
+@pytest.mark.parametrize("dtype", [q.F32, q.BF16])
+def test_norm_many_rows(T, H, group, dtype):
+    """CTAs that loop over rows, with rows that are redone or mended among the ordinary ones."""
+    rs = np.random.default_rng(T + H)
+    x = (2 * rs.standard_normal((T, H))).astype(np.float32)
+    half = np.concatenate([np.arange(-127, 128, 0.5), np.zeros(H)])[:H].astype(np.float32)
+    half[-1] = 127.0
+    x[1::7] = half                               # codes at rounding borders
+    x[2::31] *= np.float32(1e-41)
+    x[3::31] = 0
+    x[4::31, 5] = np.inf
+    x[5::31, 6] = np.nan
+    y = (rs.standard_normal((T, H)) * (rs.random((T, 1)) < 0.5)).astype(np.float32)
+    y[1::7] = 0
+    gain = dev((0.2 + rs.random(H)).astype(np.float32))
+    xd, yd = dev(x, TORCH[dtype]), dev(y, TORCH[dtype])
+    check_norm(xd, yd, dtype, gain, group)
+    check_norm(xd, None, dtype, dev(np.full(H, 1.0 / 3.0, dtype=np.float32)), group)
+    check_norm(xd, None, dtype, None, group)
 
 
 def test_norm_in_place_and_partial_outputs():
@@ -443,6 +468,53 @@ def test_sample_strides_and_largest_vocabulary():
     check_sample(l, u=uniforms(rs, 2), top_p=[0.95, 0.2], top_k=[0, 5000])
 
 
+@pytest.mark.parametrize("V", [131072, 262145, 300001])
+@pytest.mark.parametrize("dtype", [q.F32, q.BF16])
+def test_sample_large_vocabulary(V, dtype):
+    """Few rows of a large vocabulary: masked, with and without each filter, and filters that keep most of it."""
+    rs = np.random.default_rng(V + dtype)
+    T = 4
+    l = (3 * rs.standard_normal((T, V))).astype(np.float32)
+    l[1, rs.random(V) < 0.99] = -np.inf
+    l[2, rs.random(V) < 0.5] = np.finfo(np.float32).min
+    l[3] *= np.float32(0.01)                                 # flat: every filter keeps tens of thousands
+    u = uniforms(rs, T)
+    for kw in ({}, dict(min_p=[0.05, 0.1, 0.02, 0.97]), dict(top_p=[0.95] * T), dict(top_k=[40, 1000, 5000, 100000]),
+               dict(temperature=[0.7, 1.0, 2.5, 0.5], top_k=[50, 0, 2000, 0], top_p=[0.9, 0.5, 0.99, 0.9], min_p=[0, 0.01, 0, 0]),
+               dict(temperature=[0.0, 0.0, 1e-3, 0.0])):
+        check_sample(l, dtype, u=u, **kw)
+
+
+def test_sample_unaligned_rows_of_a_large_vocabulary():
+    rs = np.random.default_rng(31)
+    V, ld = 60001, 60007
+    for dtype in (q.F32, q.BF16):
+        wide = dev((2 * rs.standard_normal((3, ld))).astype(np.float32), TORCH[dtype])
+        u = uniforms(rs, 3)
+        for kw in (dict(top_p=np.float32([0.9] * 3)), dict(top_k=[50] * 3, min_p=np.float32([0.02] * 3))):
+            token, _ = run_sample(wide, dtype, ld=ld, V=V, u=u, **kw)
+            want, _ = dense.sample(f64(wide)[:, :V], u=u, **kw)
+            assert token.tolist() == want.tolist()
+
+
+@pytest.mark.parametrize("dtype", [q.F32, q.BF16])
+def test_sample_more_rows_than_sms(dtype):
+    """One CTA per row, rows of every kind among them."""
+    rs = np.random.default_rng(17 + dtype)
+    T, V = 160, 20011
+    l = (rs.uniform(0.01, 6, (T, 1)) * rs.standard_normal((T, V))).astype(np.float32)
+    l[3] = -np.inf
+    l[4, rs.random(V) < 0.999] = -np.inf
+    l[5] = 7.0
+    l[6] = np.nan
+    l[7, 100] = np.inf
+    u = uniforms(rs, T)
+    check_sample(l, dtype, u=u)
+    check_sample(l, dtype, u=u, top_p=rs.random(T))
+    check_sample(l, dtype, u=u, top_k=rs.integers(0, V, T), temperature=2 * rs.random(T))
+    check_sample(l, dtype, u=u, min_p=rs.random(T) ** 3, top_p=0.5 + 0.5 * rs.random(T), top_k=rs.integers(0, 3000, T))
+
+
 def test_sample_is_repeatable():
     rs = np.random.default_rng(9)
     l = dev((2 * rs.standard_normal((7, 60000))).astype(np.float32))
@@ -532,3 +604,75 @@ def test_two_streams_at_once():
     for d, t, (o, k) in zip(ds, toks, want):
         assert torch.equal(d["out"], o) and torch.equal(t, k)
     assert q.qmoe_read_status(st) == 0
+
+
+# ---------------------------------------------------- behind a layer stack --
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("T", [1, 8])
+def test_token_head_behind_a_stack(bits, T):
+    """Stack -> norm -> head product -> token: the same eagerly, on a side stream and captured, and the oracle's."""
+    cfg = configs.get(0).with_(L=2, T=T, residual=True)
+    layers, routers, _ = device_layers(0, cfg, 2)
+    stack = DecodeStack(layers, routers, None, T, cfg.k, cfg.eps)
+    rs = np.random.default_rng(40 + bits + T)
+    V = 5003
+    weight = dev(rs.standard_normal((V, cfg.H)).astype(np.float32), torch.bfloat16 if bits == 16 else None)
+    gain, bias = dev((0.5 + rs.random(cfg.H)).astype(np.float32)), dev(rs.standard_normal(V).astype(np.float32))
+    head = TokenHead(weight, T, gain, bias, bits=bits)
+    u = uniforms(rs, T)
+    kw = dict(temperature=np.full(T, 4.0), top_k=np.full(T, 400), top_p=np.full(T, 0.9), min_p=np.full(T, 0.001))
+    kw = {k: v.astype(np.int32 if k == "top_k" else np.float32) for k, v in kw.items()}
+    ud, kd = dev(u), {k: dev(v) for k, v in kw.items()}
+    stack.x_in.copy_(dev(gen.tokens(0, cfg, 0)))
+    stack.decode()
+    head.step(stack.x_out, ud, **kd)
+    torch.cuda.synchronize()
+    assert stack.status() == 0 and head.status() == 0
+    x = to_np(stack.x_out)
+    _, no, co, so = dense.norm_q8(x, None, to_np(gain), 1e-6, 0)
+    if bits == 8:
+        wc, ws = dense.quantise(f64(weight), 1.0, 0)
+        assert np.array_equal(to_np(head.weight), wc) and np.array_equal(to_np(head.codes), co)
+        want, pre, mag = dense.linear(co, wc, so[:, 0], ws[:, 0], f64(bias))
+        tol = (3 + 40 + 2) * U * mag + 2 * U * (np.abs(pre) + mag)
+    else:
+        want, pre, mag = dense.linear(no, f64(weight), bias=f64(bias))
+        tol = (BF + 41 * U) * mag + (cfg.H / 16 + 2) * 2 * U * mag + 2 * U * (np.abs(pre) + mag)
+    logits = f64(head.logits)
+    assert (np.abs(logits - want) <= tol).all()
+    token, prob = dense.sample(logits, u=u, **kw)
+    assert np.array_equal(to_np(head.token), token) and (np.abs(f64(head.prob) - prob) <= 2 * U * prob).all()
+
+    keep = [t.clone() for t in (head.logits, head.token, head.prob)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    for how in ("side", "graph"):
+        for t in (head.logits, head.token, head.prob):
+            t.zero_()
+        torch.cuda.synchronize()
+        if how == "side":
+            stack.decode(side)
+            head.step(stack.x_out, ud, stream=side, **kd)
+        else:
+            with torch.cuda.graph(graph):
+                head.step(stack.x_out, ud, **kd)
+            graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((head.logits, head.token, head.prob), keep):
+            assert torch.equal(a, b), how
+    stack.close()
+
+
+def test_token_head_refusals():
+    w = torch.zeros((100, 64), device="cuda")
+    for bad in (dict(weight=w[0]), dict(weight=w.double()), dict(weight=w, bits=4), dict(weight=w, T=0),
+                dict(weight=w[:, :40])):
+        with pytest.raises(q.QmoeError):
+            TokenHead(**{"T": 1, **bad})
+    head, u = TokenHead(w, 2), torch.zeros(2, device="cuda")
+    for x, uu in ((torch.zeros((1, 64), device="cuda"), u), (torch.zeros((2, 64), device="cuda").double(), u),
+                  (torch.zeros((2, 64), device="cuda"), u[:0])):
+        with pytest.raises(q.QmoeError):
+            head.step(x, uu)
+    with pytest.raises(q.QmoeError):
+        TokenHead(w, 2, gain=torch.ones(32, device="cuda")).step(torch.zeros((2, 64), device="cuda"), u)
+    assert head.step(torch.zeros((2, 64), device="cuda"), u).tolist() == [0, 0] and head.status() == 0
