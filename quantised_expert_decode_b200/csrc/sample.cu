@@ -51,7 +51,8 @@ constexpr int SQ_ROUND = 256;                 // logits of a warp whose sums are
 constexpr int SQ_LIST = 1024;                 // elements that the quick way gathers and sorts
 constexpr double SP_EPS = 1e-11;              // bound of the quick sums' error, relative to the row's sum
 constexpr int SP_LIST = SP_THREADS;           // elements ranked one by one (one per thread)
-constexpr int SP_MAX_CLUSTER = 8;
+constexpr int SP_MAX_CLUSTER = 8;             // CTAs per row in shared memory
+constexpr int SP_MAX_STREAM = 2;              // and of one that is read again and again
 constexpr int SP_MAX_SLICE = 32768;           // 128 KB of fp32 logits per CTA
 constexpr int SP_MAX_V = 393216;
 constexpr double SP_W_MIN = 5.421010862427522e-20;   // 2^-64
@@ -511,12 +512,15 @@ __device__ __forceinline__ double sq_weight(float l, const SqRow &r, const doubl
 }
 
 // The same in fp32 and y = -z: the hardware exponential (2^-22 relative) of a
-// product with three roundings (1.3e-7 of y).
+// product with three roundings, one of them that of c (c32).
+__device__ __forceinline__ float sq_exp2(float z) {
+  float w;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(z));
+  return w;
+}
 __device__ __forceinline__ float sq_fast(float l, float c32, const SqRow &r, float &y) {
   y = fminf(__fmul_rn(__fsub_rn(r.m, l), c32), 64.0f);
-  float w;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(-y));
-  return w;
+  return sq_exp2(-y);
 }
 
 // Place of a logit >= low among the bins: 11 bits of bin, 12 bits inside it.
@@ -528,6 +532,39 @@ __device__ __forceinline__ float sq_place(float l, const SqRow &r) {
 __device__ __forceinline__ unsigned sq_bin(float place) { return (__float_as_uint(place) & 0x7fffffu) >> 12; }
 // The place where bin b begins (b up to 2048).
 __device__ __forceinline__ float sq_bin_at(unsigned b) { return 8388608.0f + 4096.0f * (float)b; }
+
+// The smallest logit whose place is below `at` (+inf where there is none): a
+// guess and its neighbours, else a search by 32 parts. Whole warps; every lane gets it.
+__device__ __forceinline__ float sq_logit_at(float at, const SqRow &r) {
+  if (!(sq_place(r.m, r) < at)) return CUDART_INF_F;
+  const unsigned lane = threadIdx.x & 31, top = float_key(r.m), bottom = float_key(SP_LOWEST);
+  const float guess = fminf(fmaxf(__fsub_rn(r.m, __fdiv_rn(__fsub_rn(at, 8388608.0f), r.scale)), SP_LOWEST), r.m);
+  unsigned lo = bottom, hi = top;   // the answer's key lies in [lo, hi]
+  unsigned k = min(max(float_key(guess), bottom + 16u) - 16u + lane, top);
+  unsigned below = __ballot_sync(0xffffffffu, sq_place(key_float(k), r) < at);   // (grows with the lane)
+  if (below != 0u && below != 0xffffffffu) return key_float(__shfl_sync(0xffffffffu, k, __ffs(below) - 1));
+  for (int step = 0; step < 12 && lo < hi; ++step) {   // (7 or 8: 2^32 keys)
+    const unsigned part = (hi - lo) / 32u + 1u;
+    k = min(lo + lane * part, hi);
+    below = __ballot_sync(0xffffffffu, sq_place(key_float(k), r) < at);
+    const int f = below ? __ffs(below) - 1 : 32;   // the first part that begins with the answer or behind it
+    const unsigned from = f ? min(lo + (unsigned)(f - 1) * part, hi) + 1u : lo;
+    hi = f < 32 ? min(lo + (unsigned)f * part, hi) : hi;
+    lo = f ? from : hi;
+  }
+  return key_float(hi);
+}
+
+// Adds v to a histogram's counter where l >= hi (no branch around it).
+__device__ __forceinline__ void sq_count(uint32_t at, unsigned v, float l, float hi) {
+  asm volatile("{\n .reg .pred p;\n setp.ge.f32 p, %2, %3;\n @p red.shared.add.u32 [%0], %1;\n}" ::"r"(at), "r"(v), "f"(l), "f"(hi)
+               : "memory");
+}
+// Stores l where l >= hi, and moves on then.
+__device__ __forceinline__ void sq_stack(uint32_t &at, float l, float hi) {
+  asm volatile("{\n .reg .pred p;\n setp.ge.f32 p, %1, %2;\n @p st.shared.f32 [%0], %1;\n @p add.u32 %0, %0, 4;\n}"
+               : "+r"(at) : "f"(l), "f"(hi) : "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ void push_all(T *at, const T &v, int nc) {
@@ -653,14 +690,14 @@ __device__ __forceinline__ void sq_gather(const Src &src, SpShared *list, int i,
 
 // Top-k: everything down to rank k's bin goes to CTA 0, which finishes the row.
 template <typename Src>
-__device__ bool sq_finish_k(const Src &src, int s0, int own, int base, float hi, float end, int top_k, float top_p, float u,
+__device__ bool sq_finish_k(const Src &src, int s0, int own, int base, float from, int top_k, float top_p, float u,
                             const SqRow &r, SpShared *sh, const SpArgs &a, int t, int rank) {
   const int tid = threadIdx.x, lane = tid & 31;
   SpShared *first = dense::peer(sh, 0);
   sq_each(src, s0, own, [&](int i, const float(&l)[8]) {
     unsigned in = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) in |= l[j] >= hi && sq_place(l[j], r) < end ? 1u << j : 0u;
+    for (int j = 0; j < 8; ++j) in |= l[j] >= from ? 1u << j : 0u;
     sq_gather(src, first, s0 + i, in, base);
   });
   dense::cluster_sync();
@@ -765,6 +802,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     const float per_bin = (float)(r.c * 4096.0 / (double)r.scale);   // log2 of the weights' fall over a bin
     // a mass is 32768 at its bin's top, less by the weights' fall towards the bin's end
     const unsigned slope = (unsigned)(32768.0f * (1.0f - exp2f(-per_bin)));
+    const uint32_t bins = (uint32_t)__cvta_generic_to_shared(&sh->bins[0]);
     double s = 0.0;
     float sy = 0.0f;
     sq_each(src, s0, own, [&](int, const float(&l)[8]) {
@@ -774,22 +812,21 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
       if (k_on) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (l[j] >= hi) atomicAdd(&sh->bins[sq_bin(sq_place(l[j], r))], 1u);
+          sq_count(bins + 4 * sq_bin(sq_place(l[j], r)), 1u, l[j], hi);
         return;
       }
-      // the sum of fp32 weights beside the histogram, two at a time in fp32
+      // the sum of fp32 weights beside the histogram, two at a time in fp32 (what is
+      // left out has a weight of 2^-64 here: too small to count)
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         float w[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const bool in = l[j + k] >= hi;
-          float y;
-          w[k] = sq_fast(l[j + k], c32, r, y);
-          w[k] = in ? w[k] : 0.0f;
+          const float d = __fsub_rn(r.m, l[j + k]), y = l[j + k] >= hi ? __fmul_rn(d, c32) : 64.0f;
+          w[k] = sq_exp2(-y);
           sy = __fmaf_rn(w[k], y, sy);
-          const unsigned at = __float_as_uint(sq_place(l[j + k], r)) & 0x7fffffu;
-          if (in) atomicAdd(&sh->bins[at >> 12], ((32768u << 12) - (at & 4095u) * slope) >> 12);
+          const unsigned at = __float_as_uint(__fmaf_rn(d, r.scale, 8388608.0f));
+          sq_count(bins + (at >> 10 & 4u * (SQ_BINS - 1)), ((32768u << 12) - (at & 4095u) * slope) >> 12, l[j + k], hi);
         }
         s += (double)(w[0] + w[1]);
       }
@@ -819,12 +856,13 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     const int b0 = PER * (rank * share + tid);
     unsigned long long hh[PER] = {0, 0, 0, 0};
     if (tid < share) {
-      uint4 x[SP_MAX_CLUSTER];
+      constexpr int MOST = RES ? SP_MAX_CLUSTER : SP_MAX_STREAM;
+      uint4 x[MOST];
 #pragma unroll
-      for (int c = 0; c < (RES ? SP_MAX_CLUSTER : 1); ++c)   // all loads in flight together
+      for (int c = 0; c < MOST; ++c)   // all loads in flight together
         if (c < a.nc) x[c] = reinterpret_cast<const uint4 *>(dense::peer(&sh->bins[0], c))[b0 / 4];
 #pragma unroll
-      for (int c = 0; c < (RES ? SP_MAX_CLUSTER : 1); ++c)
+      for (int c = 0; c < MOST; ++c)
         if (c < a.nc) {
           hh[0] += x[c].x;
           hh[1] += x[c].y;
@@ -849,7 +887,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     __syncthreads();
     sq_cta_scan(__shfl_sync(0xffffffffu, incl, 31), sh->warp_d[1], before, all);
     double pre = __shfl_sync(0xffffffffu, before, wid) + incl - run;
-    if (RES) {
+    if (a.nc > 1) {
       if (tid == 0) push_all(&sh->push[5][rank], SpPush{all, 0.0, 0.0f, 0}, a.nc);
       dense::cluster_sync();
       all = 0.0;
@@ -881,49 +919,60 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     last = (unsigned)min(sh->last, SQ_BINS - 1);
     if (first >= SQ_BINS) return false;
   }
-  const float end = sq_bin_at(last + 1), open = sq_bin_at(first);   // places
-  if (k_on) return sq_finish_k(src, s0, own, base, hi, end, top_k, top_p, u, r, sh, a, t, rank);
+  // logits from `above` up lie above the open bins, from `from` up in them
+  float above = hi, from = lo;
+  if (k_on || p_on) {
+    above = fmaxf(hi, sq_logit_at(sq_bin_at(first), r));
+    from = fmaxf(hi, sq_logit_at(sq_bin_at(last + 1), r));
+  }
+  if (k_on) return sq_finish_k(src, s0, own, base, from, top_k, top_p, u, r, sh, a, t, rank);
 
   // The sum above the open bins, for each of the warp's rounds; the open bins'
-  // elements to CTA 0. Every lane stacks what it keeps of a round.
-  float *mine = stack + wid * SQ_ROUND + lane;
+  // elements to CTA 0. What is kept of a round is stacked, lane behind lane.
+  const float *mine = stack + wid * SQ_ROUND;
+  const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(mine);
   SpShared *lists = dense::peer(sh, 0);
   double ws = 0.0, a_fast = 0.0;   // exact weights; fp32 weights of the same
   float a_sy = 0.0f;
   sq_each(src, s0, own, [&](int i, const float(&l)[8]) {
     int held = 0;   // of this lane
-    unsigned opens = 0;
+    float rest = -CUDART_INF_F;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      bool in = l[j] >= hi;
-      if (p_on) {
-        const float place = sq_place(l[j], r);
-        opens |= in && place >= open && place < end ? 1u << j : 0u;
-        in = in && place < open;
-      } else {
-        bad |= l[j] >= lo && !in;
-      }
-      if (in) mine[32 * held++] = l[j];
+      const bool in = l[j] >= above;
+      held += in ? 1 : 0;
+      rest = fmaxf(rest, in ? -CUDART_INF_F : l[j]);
     }
-    if (opens) sq_gather(src, lists, s0 + i, opens, base);
-    const int most = __reduce_max_sync(0xffffffffu, held);
+    if (rest >= from) {
+      bad |= !p_on;   // min-p alone leaves nothing open
+      unsigned opens = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) opens |= l[j] >= from && l[j] < above ? 1u << j : 0u;
+      if (p_on) sq_gather(src, lists, s0 + i, opens, base);
+    }
+    int upto = held;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      upto += lane >= o ? y : 0;
+    }
+    const int all = __shfl_sync(0xffffffffu, upto, 31);
+    uint32_t at = mine_at + 4 * (upto - held);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sq_stack(at, l[j], above);
+    __syncwarp();
     double x = 0.0;
 #pragma unroll 1
-    for (int k = 0; k < most; k += 2) {   // (behind a lane's own: stale logits, not counted)
-      double w[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool in = k + j < held;
-        const float m2 = mine[32 * (k + j)];
-        w[j] = sq_weight(in ? m2 : -CUDART_INF_F, r, sh->exp2_tab);
-        float y, v = sq_fast(m2, c32, r, y);
-        v = in ? v : 0.0f;
-        a_fast += (double)v;
-        a_sy = in ? __fmaf_rn(v, y, a_sy) : a_sy;
-      }
-      x += w[0] + w[1];
+    for (int k = lane; k - lane < all; k += 32) {
+      const float v = k < all ? mine[k] : -CUDART_INF_F;
+      x += sq_weight(v, r, sh->exp2_tab);
+      float y;
+      const float w = sq_fast(v, c32, r, y);   // (2^-64 where there is none)
+      a_fast += (double)w;
+      a_sy = __fmaf_rn(w, y, a_sy);
     }
-    x = most ? warp_sum_d(x) : 0.0;
+    __syncwarp();
+    x = all ? warp_sum_d(x) : 0.0;
     if (lane == 0) sh->rounds[wid][i / SQ_ROUND] = x;
     ws += x;
   });
@@ -953,8 +1002,9 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     const int listed = (int)lists->list_n;
     if (listed > SQ_LIST) return false;
     // The row's sum: exact weights down to the open bins, fp32 weights below
-    // them. Its error: 1.4e-7 of y and 2.4e-7 of each weight below, and the
-    // roundings of two weights added in fp32 of the whole first sum.
+    // them, freed of what c's fp32 value is off by (y times that, relatively). Its
+    // error: two roundings of y (9e-8 of it) and 2.4e-7 of each weight below, and
+    // the roundings of two weights added in fp32 of the whole first sum.
     double whole = total + S, err = 0.0;
     if (rank == 0) {
       sq_rank(sh, listed, r);
@@ -973,8 +1023,9 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
       open_sy = (float)sq_cta_sum((double)warp_sum(open_sy), sh->warp_d[0]);
       S -= open_fast;
       SY -= (double)open_sy;
+      S += 0.6931471805599453 * ((double)c32 - r.c) / r.c * SY;
       whole = total + open_sum + S;
-      err = p * (1.4e-7 * fmax(SY, 0.0) + 2.6e-7 * fmax(S, 0.0) + 8e-8 * whole);
+      err = p * (9e-8 * fmax(SY, 0.0) + 2.6e-7 * fmax(S, 0.0) + 8e-8 * whole);
     }
     for (int round = 0; round < 2; ++round) {   // (uniform over the cluster)
       if (rank == 0 && tid < 32) {
@@ -1155,7 +1206,7 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SpArgs a) {
   float *stack = reinterpret_cast<float *>(sp_smem + sp_head_bytes());   // a round's logits per warp
   float *vals = stack + SP_WARPS * SQ_ROUND;                             // RES: the slice
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int rank = RES ? (int)dense::cluster_rank() : 0, t = blockIdx.x / a.nc;
+  const int rank = (int)dense::cluster_rank(), t = blockIdx.x / a.nc;
   const int base = min(a.V, rank * a.slice), n = min(a.V, base + a.slice) - base;
 
   const float temp = a.temperature ? a.temperature[t] : 1.0f;
@@ -1333,6 +1384,8 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   int nc = 1;
   if (res)
     while (nc < SP_MAX_CLUSTER && ((V + nc - 1) / nc > SP_MAX_SLICE / 2 || (long long)T * nc * 2 <= sms)) nc *= 2;
+  else if (V * (dtype == QMOE_BF16 ? 2 : 4) > 200 * 1024)
+    nc = SP_MAX_STREAM;
   const int slice = ((V + nc - 1) / nc + 7) / 8 * 8;
   const int seg = (slice + SP_WARPS * 128 - 1) / (SP_WARPS * 128) * 128;
   const size_t smem = sp_head_bytes() + (size_t)SP_WARPS * (SQ_ROUND + (res ? seg : 0)) * 4;
