@@ -25,6 +25,35 @@ size_t max_smem_optin() {
   return (size_t)n;
 }
 
+namespace dense {
+
+int max_clusters(int size, const void *fn, int threads, int smem) {
+  static std::atomic<int> known[16][MAX_CLUSTER + 1];
+  int dev = 0;
+  if (size < 1 || size > MAX_CLUSTER || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return 0;
+  int n = known[dev][size].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return 0;
+    }
+    known[dev][size].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+}  // namespace dense
 }  // namespace qmoe
 
 extern "C" uint64_t qmoe_launch_count(void) { return qmoe::g_launches.load(); }

@@ -14,6 +14,13 @@ constexpr int32_t DEV_BAD_PARAM = 5;   // a per-row parameter read on the device
 
 namespace dense {
 
+// Clusters of `size` CTAs that run at once on the current device, for kernels whose
+// CTAs take an SM each, as `fn` with these threads and shared memory does (a cluster lies within one part of
+// the chip: 16 clusters of 8 do not fit on 148 SMs, and a second wave costs more than
+// fewer CTAs). 0 where that cannot be told.
+constexpr int MAX_CLUSTER = 8;
+int max_clusters(int size, const void *fn, int threads, int smem);
+
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void *p = nullptr;

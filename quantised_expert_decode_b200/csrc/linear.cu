@@ -712,35 +712,9 @@ const void *ln_kernel(bool i8, bool f32) {
   return (const void *)linear_kernel<MODE, BT, false, false>;
 }
 
-// Clusters of `size` CTAs, one CTA per SM, that run at once on this device (a
-// cluster lies within one part of the chip: 16 clusters of 8 do not fit on 148
-// SMs, and a second wave costs more than a narrower split).
 int ln_max_clusters(int size) {
-  static std::atomic<int> known[16][LN_MAX_SPLIT + 1];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return 0;
-  int n = known[dev][size].load(std::memory_order_relaxed);
-  if (n == 0) {
-    const void *fn = (const void *)linear_kernel<LN_FEATURES, 16, true, false>;
-    const int smem = ln_smem_bytes(LN_FEATURES, 16);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(size);
-    cfg.blockDim = dim3(ln_threads(LN_FEATURES, 16));
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = size;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      return 0;
-    }
-    known[dev][size].store(n, std::memory_order_relaxed);
-  }
-  return n;
+  return dense::max_clusters(size, (const void *)linear_kernel<LN_FEATURES, 16, true, false>, ln_threads(LN_FEATURES, 16),
+                             ln_smem_bytes(LN_FEATURES, 16));
 }
 
 qmoe_status ln_launch(const void *fn, int smem, int threads, const LnArgs &a, int grid, int cluster, cudaStream_t s) {

@@ -13,8 +13,13 @@
 //
 // Where the row lives: few rows are each spread over a cluster of CTAs, every
 // CTA with a contiguous slice of the row in shared memory (`RES`; one read from
-// HBM). Many rows are taken by one CTA each, which reads its row three times,
-// twice out of L2: no cluster barriers, and enough rows in flight.
+// HBM). Many rows are read three times, twice out of L2, by two CTAs per SM; each
+// row by as many of them as there are to spare.
+// Bound: for few rows the chain of its steps (some ten cluster barriers and as
+// many short sums of a few hundred cycles each: 1 x 131072 with top-k, top-p and
+// min-p 16 us, 8 x 131072 bf16 with top-p 35 us); for many the issue of some 65
+// instructions per logit (256 x 131072 fp32 with top-p 140 us, 15 % of the
+// measured copy rate).
 //
 // How the border is found:
 // quick - one pass builds a histogram over 2048 value bins (counts for top-k,
@@ -50,9 +55,9 @@ constexpr int SQ_BINS = 2048;                 // quick way: 11 bits of bin, 12 b
 constexpr int SQ_ROUND = 256;                 // logits of a warp whose sums are kept apart: two float4 per lane
 constexpr int SQ_LIST = 1024;                 // elements that the quick way gathers and sorts
 constexpr double SP_EPS = 1e-11;              // bound of the quick sums' error, relative to the row's sum
-constexpr int SP_LIST = SP_THREADS;           // elements ranked one by one (one per thread)
-constexpr int SP_MAX_CLUSTER = 8;             // CTAs per row in shared memory
-constexpr int SP_MAX_STREAM = 2;              // and of one that is read again and again
+constexpr int SP_LIST = 512;                  // elements ranked one by one (one per thread)
+constexpr int SP_MAX_CLUSTER = 8;             // CTAs per row
+constexpr long long SP_L2_BYTES = 126ll << 20;
 constexpr int SP_MAX_SLICE = 32768;           // 128 KB of fp32 logits per CTA
 constexpr int SP_MAX_V = 393216;
 constexpr double SP_W_MIN = 5.421010862427522e-20;   // 2^-64
@@ -69,7 +74,7 @@ struct SpArgs {
   int32_t *status;
   long long ld;
   int T, V, slice, nc;       // nc: CTAs per row
-  int seg;                   // a warp's part of the slice, a multiple of 128
+  int seg, rounds;           // a warp's part of the slice, a multiple of 128, and its rounds
 };
 
 // What one CTA contributes to a step of the exact way.
@@ -83,7 +88,7 @@ struct SpPart {
 struct SpPush {
   double a, b;
   float c;
-  int bad;
+  int bad, listed, pad;
 };
 
 struct SpShared {
@@ -107,13 +112,14 @@ struct SpShared {
     };
     unsigned long long keys[SQ_LIST];         // quick way: sq_key of gathered elements
   };
-  double rounds[SP_WARPS][SP_MAX_V / SP_WARPS / SQ_ROUND];
+  double rounds[SP_MAX_V / SQ_ROUND];           // a warp's rounds are neighbours
   unsigned int list_n;
   int found, last;
   float border_v;
   int border_i, bad;
   double open_sum;
   float live, q_lo, q_hi;
+  double log_min_p;
 };
 
 static_assert(offsetof(SpShared, bins) % 16 == 0 && alignof(SpShared) == 16, "bins are read as uint4");
@@ -493,6 +499,17 @@ struct SqRow {
   float scale;      // bins: place = (m - l) * scale, in [0, 2^23) from `low` up
 };
 
+__device__ const double SQ_EXP2[32] = {   // 2^(i / 32)
+    1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
+    1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
+    1.189207115002721, 1.215247359980469, 1.241857812073484, 1.2690509571917332,
+    1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228,
+    1.5422108254079407, 1.5759808451078865, 1.6104903319492543, 1.645755478153965,
+    1.681792830507429, 1.718619298122478, 1.7562521603732995, 1.7947090750031072,
+    1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002,
+};
+
 // 2^z for z = (l - m) log2(e) / temperature: z to the nearest 1/32, a table for
 // that and the Taylor polynomial of degree 4 for the rest (|r| <= 1/64, so the
 // next term is below (ln2 / 64)^5 / 120 = 1.3e-12).
@@ -678,31 +695,51 @@ __device__ __forceinline__ void sq_each(const Src &src, int s0, int own, F f) {
   }
 }
 
-// The lane's elements (as sq_each gives them) whose bits are set, to a list.
+// The lane's elements (as sq_each gives them) whose bits are set, to the CTA's list.
 template <typename Src>
-__device__ __forceinline__ void sq_gather(const Src &src, SpShared *list, int i, unsigned bits, int base) {
+__device__ __forceinline__ void sq_gather(const Src &src, SpShared *sh, int i, unsigned bits, int base) {
   for (; bits; bits &= bits - 1) {
     const int j = __ffs(bits) - 1, e = i + 4 * (threadIdx.x & 31) + (j & 3) + 32 * (j & 4);
-    const unsigned k = atomicAdd(&list->list_n, 1u);
-    if (k < SQ_LIST) list->keys[k] = sq_key(src.at(e), base + e);
+    const unsigned k = atomicAdd(&sh->list_n, 1u);
+    if (k < SQ_LIST) sh->keys[k] = sq_key(src.at(e), base + e);
   }
 }
 
+// CTA 0 fetches what the others have listed behind its own list (their counts came
+// with `push`, before the last cluster barrier), unless it is too much. All threads; the
+// count of all CTAs' elements. (Listing straight into CTA 0's memory, a remote atomic
+// per element, held up its rounds, and read by CTA 0 alone it needs no barrier.)
+__device__ int sq_collect(SpShared *sh, const SpPush *push, const SpArgs &a, int rank) {
+  int all = 0;
+  for (int c = 0; c < a.nc; ++c) all += push[c].listed;
+  if (rank == 0 && all <= SQ_LIST) {
+    int from = push[0].listed;
+    for (int c = 1; c < a.nc; ++c) {
+      const SpShared *o = dense::peer(sh, c);
+      for (int i = threadIdx.x; i < push[c].listed; i += SP_THREADS) sh->keys[from + i] = o->keys[i];
+      from += push[c].listed;
+    }
+    __syncthreads();
+  }
+  return all;
+}
+
 // Top-k: everything down to rank k's bin goes to CTA 0, which finishes the row.
-template <typename Src>
-__device__ bool sq_finish_k(const Src &src, int s0, int own, int base, float from, int top_k, float top_p, float u,
+template <bool BF16, bool RES>
+__device__ bool sq_finish_k(const SpSrc<BF16, RES> &src, int s0, int own, int base, float from, int top_k, float top_p, float u,
                             const SqRow &r, SpShared *sh, const SpArgs &a, int t, int rank) {
   const int tid = threadIdx.x, lane = tid & 31;
-  SpShared *first = dense::peer(sh, 0);
   sq_each(src, s0, own, [&](int i, const float(&l)[8]) {
     unsigned in = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) in |= l[j] >= from ? 1u << j : 0u;
-    sq_gather(src, first, s0 + i, in, base);
+    sq_gather(src, sh, s0 + i, in, base);
   });
+  __syncthreads();
+  if (tid == 0) push_all(&sh->push[1][rank], SpPush{0.0, 0.0, 0.0f, 0, (int)sh->list_n, 0}, a.nc);
   dense::cluster_sync();
+  int kept = sq_collect(sh, sh->push[1], a, rank);
   if (rank == 0) {
-    int kept = (int)sh->list_n;
     bool good = kept <= SQ_LIST;
     if (good) {
       sq_rank(sh, kept, r);
@@ -732,15 +769,16 @@ __device__ bool sq_finish_k(const Src &src, int s0, int own, int base, float fro
       __syncthreads();
       kept = sh->warp_i[0];
       // by index: the kept elements as (index, rank)
-      unsigned long long mine[SQ_LIST / SP_THREADS];
+      constexpr int EACH = SQ_LIST / SP_THREADS;
+      unsigned long long mine[EACH];
 #pragma unroll
-      for (int c = 0; c < SQ_LIST / SP_THREADS; ++c) {
+      for (int c = 0; c < EACH; ++c) {
         const int j = c * SP_THREADS + tid;
         mine[c] = j < kept ? (sh->keys[j] << 32) | (unsigned)j : ~0ull;
       }
       __syncthreads();
 #pragma unroll
-      for (int c = 0; c < SQ_LIST / SP_THREADS; ++c) sh->keys[c * SP_THREADS + tid] = mine[c];
+      for (int c = 0; c < EACH; ++c) sh->keys[c * SP_THREADS + tid] = mine[c];
       sq_sort(sh, kept);
       if (tid < 32) {
         const double tot = sh->warp_d[0][0];
@@ -778,11 +816,10 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
   if (!(range > 0.0f && r.scale < 1e30f && r.scale > 1e-30f && r.c < 1e30 && r.c > 1e-30)) return false;
   // min-p: kept from `hi` up, undecided from `lo` up
   if (mp_on && tid == 0) {
-    const double at = (double)m + (double)temp * log((double)min_p), d = 1e-10 * (double)temp + 1e-14 * fabs(at);
+    const double at = (double)m + (double)temp * sh->log_min_p, d = 1e-10 * (double)temp + 1e-14 * fabs(at);
     sh->q_hi = __double2float_ru(at + d);
     sh->q_lo = __double2float_ru(at - d);
   }
-  if (tid >= SP_THREADS - 32) sh->exp2_tab[lane] = exp2((double)lane * 0.03125);
   if (k_on || p_on)
     for (int i = tid; i < SQ_BINS; i += SP_THREADS) sh->bins[i] = 0;
   __syncthreads();
@@ -856,13 +893,12 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     const int b0 = PER * (rank * share + tid);
     unsigned long long hh[PER] = {0, 0, 0, 0};
     if (tid < share) {
-      constexpr int MOST = RES ? SP_MAX_CLUSTER : SP_MAX_STREAM;
-      uint4 x[MOST];
+      uint4 x[SP_MAX_CLUSTER];
 #pragma unroll
-      for (int c = 0; c < MOST; ++c)   // all loads in flight together
+      for (int c = 0; c < SP_MAX_CLUSTER; ++c)   // all loads in flight together
         if (c < a.nc) x[c] = reinterpret_cast<const uint4 *>(dense::peer(&sh->bins[0], c))[b0 / 4];
 #pragma unroll
-      for (int c = 0; c < MOST; ++c)
+      for (int c = 0; c < SP_MAX_CLUSTER; ++c)
         if (c < a.nc) {
           hh[0] += x[c].x;
           hh[1] += x[c].y;
@@ -931,7 +967,6 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
   // elements to CTA 0. What is kept of a round is stacked, lane behind lane.
   const float *mine = stack + wid * SQ_ROUND;
   const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(mine);
-  SpShared *lists = dense::peer(sh, 0);
   double ws = 0.0, a_fast = 0.0;   // exact weights; fp32 weights of the same
   float a_sy = 0.0f;
   sq_each(src, s0, own, [&](int i, const float(&l)[8]) {
@@ -948,7 +983,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
       unsigned opens = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) opens |= l[j] >= from && l[j] < above ? 1u << j : 0u;
-      if (p_on) sq_gather(src, lists, s0 + i, opens, base);
+      if (p_on) sq_gather(src, sh, s0 + i, opens, base);
     }
     int upto = held;
 #pragma unroll
@@ -973,7 +1008,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     }
     __syncwarp();
     x = all ? warp_sum_d(x) : 0.0;
-    if (lane == 0) sh->rounds[wid][i / SQ_ROUND] = x;
+    if (lane == 0) sh->rounds[wid * a.rounds + i / SQ_ROUND] = x;
     ws += x;
   });
   bad = __syncthreads_or(bad);
@@ -984,7 +1019,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     __syncthreads();
     a_sy = (float)sq_cta_sum((double)warp_sum(a_sy), sh->warp_d[1]);
   }
-  if (tid == 0) push_all(&sh->push[1][rank], SpPush{sum, a_fast, a_sy, bad}, a.nc);
+  if (tid == 0) push_all(&sh->push[1][rank], SpPush{sum, a_fast, a_sy, bad, (int)sh->list_n, 0}, a.nc);
   dense::cluster_sync();
   double total = 0.0;
   for (int c = 0; c < a.nc; ++c) {
@@ -999,7 +1034,8 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
   int bi = a.V;
   if (p_on) {
     const double p = (double)fmaxf(top_p, 0.0f);
-    const int listed = (int)lists->list_n;
+    const SpShared *lists = dense::peer(sh, 0);
+    const int listed = sq_collect(sh, sh->push[1], a, rank);
     if (listed > SQ_LIST) return false;
     // The row's sum: exact weights down to the open bins, fp32 weights below
     // them, freed of what c's fp32 value is off by (y times that, relatively). Its
@@ -1069,11 +1105,11 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     // sums decide is checked against SP_EPS, so their order does not matter)
     for (int j = tid; j <= sh->found; j += SP_THREADS) {
       const int i = (int)(unsigned)lists->keys[j] - base;
-      if (i >= 0 && i < n) atomicAdd(&sh->rounds[i / a.seg][i % a.seg / SQ_ROUND], lists->w[j]);
+      if (i >= 0 && i < n) atomicAdd(&sh->rounds[i / a.seg * a.rounds + i % a.seg / SQ_ROUND], lists->w[j]);
     }
     __syncthreads();
     ws = 0.0;
-    for (int i = lane; i * SQ_ROUND < own; i += 32) ws += sh->rounds[wid][i];
+    for (int i = lane; i * SQ_ROUND < own; i += 32) ws += sh->rounds[wid * a.rounds + i];
     ws = warp_sum_d(ws);
     sq_cta_scan(ws, sh->warp_d[1], warps_before, sum);
     if (tid == 0) push_all(&sh->push[3][rank], SpPush{sum, 0.0, 0.0f, 0}, a.nc);
@@ -1113,7 +1149,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
       int i0 = 0;
       for (int k = 0; k < own; k += 32 * SQ_ROUND) {
         const int i = k + lane * SQ_ROUND;
-        const double own_r = i < own ? sh->rounds[wid][i / SQ_ROUND] : 0.0, z = scan(own_r);
+        const double own_r = i < own ? sh->rounds[wid * a.rounds + i / SQ_ROUND] : 0.0, z = scan(own_r);
         const unsigned pass = __ballot_sync(0xffffffffu, own_r > 0.0 && b2 + z > aim);
         if (pass) {
           const int c = __ffs(pass) - 1;
@@ -1200,7 +1236,7 @@ __device__ void sp_load(const SpSrc<BF16, RES> &src, float *vals, int padded, fl
 }
 
 template <bool BF16, bool RES>
-__global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SpArgs a) {
+__global__ void __launch_bounds__(SP_THREADS, RES ? 1 : 2) sample_kernel(SpArgs a) {
   extern __shared__ __align__(16) uint8_t sp_smem[];
   SpShared *sh = reinterpret_cast<SpShared *>(sp_smem);
   float *stack = reinterpret_cast<float *>(sp_smem + sp_head_bytes());   // a round's logits per warp
@@ -1218,7 +1254,11 @@ __global__ void __launch_bounds__(SP_THREADS, 2) sample_kernel(SpArgs a) {
   const void *row = static_cast<const uint8_t *>(a.logits) + ((size_t)t * a.ld + base) * (BF16 ? 2 : 4);
   const SpSrc<BF16, RES> src{row, vals, n, (reinterpret_cast<uintptr_t>(row) & (BF16 ? 7 : 15)) == 0};
   float mx, mn;
+  if (wid == SP_WARPS - 1) {   // beside the others' loads
+    if (lane == 0) sh->log_min_p = min_p > 0.0f ? log((double)min_p) : 0.0;
+  }
   sp_load(src, vals, SP_WARPS * a.seg, mx, mn);
+  if (tid < 32) sh->exp2_tab[tid] = SQ_EXP2[tid];
   mx = warp_max(mx);
   mn = -warp_max(-mn);
   if (lane == 0) {
@@ -1378,22 +1418,32 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
                        reinterpret_cast<uintptr_t>(prob) | reinterpret_cast<uintptr_t>(dev_status);
   if ((a4 & 3) || !aligned16(logits)) return QMOE_ERR_INVALID_ARG;
   if (V > SP_MAX_V || T > (1 << 27)) return QMOE_ERR_UNSUPPORTED;
-  // many rows: one CTA each; few rows: enough CTAs to hold a row, then enough to fill the machine
+  const auto smem_of = [](bool res, int seg) { return (int)(sp_head_bytes() + (size_t)SP_WARPS * (SQ_ROUND + (res ? seg : 0)) * 4); };
+  const auto kernel = [&](bool res) {
+    return dtype == QMOE_BF16 ? (res ? (const void *)sample_kernel<true, true> : (const void *)sample_kernel<true, false>)
+                              : (res ? (const void *)sample_kernel<false, true> : (const void *)sample_kernel<false, false>);
+  };
+  // In shared memory, by as many CTAs per row as run at once, where they can hold it
+  // (131072 fp32 logits, top-p: 12 rows by 8 CTAs 30 us, 18 to 30 rows by 4 33 us, where
+  // 8, in two turns, take 46 and reading again and again 38). Else two CTAs per SM read rows
+  // out of L2 (40 rows 50 us, in shared memory in turns 75; 73 rows 67 and 124), and at
+  // least two per row where the rows under way do not fit there (256 rows of 131072:
+  // 139 us, one each 148; of 60000: one each 72 us, two 82).
   const int sms = num_sms();
-  const bool res = T < sms / 2 && V <= SP_MAX_CLUSTER * SP_MAX_SLICE;
-  int nc = 1;
-  if (res)
-    while (nc < SP_MAX_CLUSTER && ((V + nc - 1) / nc > SP_MAX_SLICE / 2 || (long long)T * nc * 2 <= sms)) nc *= 2;
-  else if (V * (dtype == QMOE_BF16 ? 2 : 4) > 200 * 1024)
-    nc = SP_MAX_STREAM;
+  int nc = SP_MAX_CLUSTER;
+  while (nc > 1 && (T * (long long)nc > sms || T > dense::max_clusters(nc, kernel(true), SP_THREADS, smem_of(true, SP_MAX_SLICE / SP_WARPS)))) nc /= 2;
+  const bool res = T <= sms && (V + nc - 1) / nc <= SP_MAX_SLICE;
+  if (!res) {
+    nc = 1;
+    while (nc < SP_MAX_CLUSTER && T * (long long)nc <= sms) nc *= 2;
+    if (nc == 1 && 2LL * sms * V * (dtype == QMOE_BF16 ? 2 : 4) > SP_L2_BYTES) nc = 2;
+  }
   const int slice = ((V + nc - 1) / nc + 7) / 8 * 8;
   const int seg = (slice + SP_WARPS * 128 - 1) / (SP_WARPS * 128) * 128;
-  const size_t smem = sp_head_bytes() + (size_t)SP_WARPS * (SQ_ROUND + (res ? seg : 0)) * 4;
-  if (smem > max_smem_optin()) return QMOE_ERR_UNSUPPORTED;
-  SpArgs args{logits, temperature, top_p, min_p, u, top_k, token, prob, dev_status, ld, T, V, slice, nc, seg};
-  const void *fn = dtype == QMOE_BF16 ? (res ? (const void *)sample_kernel<true, true> : (const void *)sample_kernel<true, false>)
-                                      : (res ? (const void *)sample_kernel<false, true> : (const void *)sample_kernel<false, false>);
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  const int smem = smem_of(res, seg);
+  SpArgs args{logits, temperature, top_p, min_p, u, top_k, token, prob, dev_status, ld, T, V, slice, nc, seg, (seg + SQ_ROUND - 1) / SQ_ROUND};
+  const void *fn = kernel(res);
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return QMOE_ERR_CUDA;
   void *params[] = {&args};
   cudaLaunchConfig_t cfg{};
