@@ -17,8 +17,8 @@
 // row by as many of them as there are to spare.
 // Bound: for few rows the chain of its steps (some ten cluster barriers and as
 // many short sums of a few hundred cycles each: 1 x 131072 with top-k, top-p and
-// min-p 16 us, 8 x 131072 bf16 with top-p 35 us); for many the issue of some 65
-// instructions per logit (256 x 131072 fp32 with top-p 140 us, 15 % of the
+// min-p 16 us, 8 x 131072 bf16 with top-p 33 us); for many the issue of some 65
+// instructions per logit (256 x 131072 fp32 with top-p 137 us, 15 % of the
 // measured copy rate).
 //
 // How the border is found:
@@ -51,7 +51,8 @@ namespace {
 constexpr int SP_THREADS = 512;
 constexpr int SP_WARPS = SP_THREADS / 32;
 constexpr int SP_BINS = 1024;                 // exact way
-constexpr int SQ_BINS = 2048;                 // quick way: 11 bits of bin, 12 bits of place within it
+constexpr int SQ_BINS = 2048;                 // quick way: 11 bits of bin, 12 bits of place within it (4096 bins: 6 % slower)
+constexpr int SQ_SUB = 12;
 constexpr int SQ_ROUND = 256;                 // logits of a warp whose sums are kept apart: two float4 per lane
 constexpr int SQ_LIST = 1024;                 // elements that the quick way gathers and sorts
 constexpr double SP_EPS = 1e-11;              // bound of the quick sums' error, relative to the row's sum
@@ -136,18 +137,21 @@ struct SpSrc {
     if (RES) return vals[i];
     return BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[i]) : static_cast<const float *>(row)[i];
   }
-  // Four neighbours from i (a multiple of 4); -inf from `end` on.
+  // Four neighbours from i (a multiple of 4) within a slice whose `vec` holds.
+  __device__ __forceinline__ float4 all_four(int i) const {
+    if (RES) return *reinterpret_cast<const float4 *>(vals + i);
+    if (!BF16) return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + i));
+    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(row) + i));
+    return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                       __uint_as_float(q.y & 0xffff0000u));
+  }
+  // The same, -inf from `end` on.
   __device__ __forceinline__ float4 four(int i, int end) const {
     if (RES) {
       if (i >= end) return make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
-      return *reinterpret_cast<const float4 *>(vals + i);   // -inf behind the slice
+      return all_four(i);   // -inf behind the slice
     }
-    if (vec && i + 4 <= end) {
-      if (!BF16) return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + i));
-      const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(row) + i));
-      return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
-                         __uint_as_float(q.y & 0xffff0000u));
-    }
+    if (vec && i + 4 <= end) return all_four(i);
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = i + j < end ? at(i + j) : -CUDART_INF_F;
@@ -546,9 +550,9 @@ __device__ __forceinline__ float sq_fast(float l, float c32, const SqRow &r, flo
 __device__ __forceinline__ float sq_place(float l, const SqRow &r) {
   return __fmaf_rn(__fsub_rn(r.m, l), r.scale, 8388608.0f);
 }
-__device__ __forceinline__ unsigned sq_bin(float place) { return (__float_as_uint(place) & 0x7fffffu) >> 12; }
-// The place where bin b begins (b up to 2048).
-__device__ __forceinline__ float sq_bin_at(unsigned b) { return 8388608.0f + 4096.0f * (float)b; }
+__device__ __forceinline__ unsigned sq_bin(float place) { return (__float_as_uint(place) & 0x7fffffu) >> SQ_SUB; }
+// The place where bin b begins (b up to SQ_BINS).
+__device__ __forceinline__ float sq_bin_at(unsigned b) { return 8388608.0f + (float)(1 << SQ_SUB) * (float)b; }
 
 // The smallest logit whose place is below `at` (+inf where there is none): a
 // guess and its neighbours, else a search by 32 parts. Whole warps; every lane gets it.
@@ -682,15 +686,24 @@ __device__ __forceinline__ double sq_cta_sum(double v, double *buf) {
 // f(i, l): a warp's part of a row in rounds of 256, i the place of the round in
 // the part. Lane's elements: l[0..3] at i + 4 lane, l[4..7] at i + 128 + 4 lane;
 // -inf behind the part. The next round's loads are under way meanwhile.
-template <typename Src, typename F>
-__device__ __forceinline__ void sq_each(const Src &src, int s0, int own, F f) {
-  const int at = s0 + 4 * (threadIdx.x & 31), end = s0 + own;
-  float4 a = src.four(at, end), b = src.four(at + 128, end);
+template <bool BF16, bool RES, typename F>
+__device__ __forceinline__ void sq_each(const SpSrc<BF16, RES> &src, int s0, int own, F f) {
+  const int at = s0 + 4 * (threadIdx.x & 31), end = s0 + own, easy = RES || src.vec ? own - SQ_ROUND : -1;
+  float4 a, b;
+  auto fetch = [&](int i) {
+    if (i <= easy) {   // (a whole round)
+      a = src.all_four(at + i);
+      b = src.all_four(at + i + 128);
+    } else {
+      a = src.four(at + i, end);
+      b = src.four(at + i + 128, end);
+    }
+  };
+  fetch(0);
 #pragma unroll 1
   for (int i = 0; i < own; i += SQ_ROUND) {
     const float l[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    a = src.four(at + i + SQ_ROUND, end);
-    b = src.four(at + i + SQ_ROUND + 128, end);
+    fetch(i + SQ_ROUND);
     f(i, l);
   }
 }
@@ -811,7 +824,12 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
   // weights below 2^-63.9 are left out (their sum stays far below SP_EPS)
   const double cut = (double)m - 44.29 * (double)temp;
   r.cut = cut > (double)SP_LOWEST ? __double2float_ru(cut) : SP_LOWEST;
-  const float range = __fsub_rn(m, fmaxf(lmin, r.cut));
+  // top-p: what lies below `tail` weighs less than 1 - top_p in all, and the row's sum is
+  // at least 1, so the border is above and the bins need not reach further
+  const float few = fmaxf(1.0f - fmaxf(top_p, 0.0f), 5e-8f);
+  const double tail = k_on || !p_on ? (double)r.cut : (double)m - (double)temp * 0.6932 * (double)(__log2f((float)a.V / few) + 0.01f);
+  const float low = fmaxf(fmaxf(lmin, r.cut), tail > (double)SP_LOWEST ? __double2float_rd(tail) : SP_LOWEST);
+  const float range = __fsub_rn(m, low);
   r.scale = __fdiv_rn(8380000.0f, range);   // a little below 2^23 / range
   if (!(range > 0.0f && r.scale < 1e30f && r.scale > 1e-30f && r.c < 1e30 && r.c > 1e-30)) return false;
   // min-p: kept from `hi` up, undecided from `lo` up
@@ -828,6 +846,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     lo = fmaxf(lo, sh->q_lo);
     hi = fminf(fmaxf(hi, sh->q_hi), m);   // the largest logit is always kept
   }
+  const float counted = fmaxf(hi, low);                 // these have a bin
   const int s0 = wid * a.seg;                           // this warp's part, in index order
   const int own = max(0, min(n, s0 + a.seg) - s0);      // elements of it
   int bad = 0;
@@ -836,7 +855,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
   unsigned first = SQ_BINS, last = SQ_BINS - 1;   // the border lies in these bins
   double S = 0.0, SY = 0.0;   // the row's sum of fp32 weights, and of weights times y
   if (k_on || p_on) {
-    const float per_bin = (float)(r.c * 4096.0 / (double)r.scale);   // log2 of the weights' fall over a bin
+    const float per_bin = (float)(r.c * (double)(1 << SQ_SUB) / (double)r.scale);   // log2 of the weights' fall over a bin
     // a mass is 32768 at its bin's top, less by the weights' fall towards the bin's end
     const unsigned slope = (unsigned)(32768.0f * (1.0f - exp2f(-per_bin)));
     const uint32_t bins = (uint32_t)__cvta_generic_to_shared(&sh->bins[0]);
@@ -849,7 +868,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
       if (k_on) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          sq_count(bins + 4 * sq_bin(sq_place(l[j], r)), 1u, l[j], hi);
+          sq_count(bins + 4 * sq_bin(sq_place(l[j], r)), 1u, l[j], counted);
         return;
       }
       // the sum of fp32 weights beside the histogram, two at a time in fp32 (what is
@@ -863,7 +882,8 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
           w[k] = sq_exp2(-y);
           sy = __fmaf_rn(w[k], y, sy);
           const unsigned at = __float_as_uint(__fmaf_rn(d, r.scale, 8388608.0f));
-          sq_count(bins + (at >> 10 & 4u * (SQ_BINS - 1)), ((32768u << 12) - (at & 4095u) * slope) >> 12, l[j + k], hi);
+          sq_count(bins + (at >> (SQ_SUB - 2) & 4u * (SQ_BINS - 1)),
+                   ((32768u << SQ_SUB) - (at & ((1u << SQ_SUB) - 1u)) * slope) >> SQ_SUB, l[j + k], counted);
         }
         s += (double)(w[0] + w[1]);
       }
@@ -888,23 +908,26 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     // every CTA adds its share of the bins over the cluster (PER neighbouring
     // bins per thread), then the shares' sums go round
     constexpr int PER = SQ_BINS / SP_THREADS;
-    static_assert(PER == 4, "one uint4 of bins per thread");
+    static_assert(PER % 4 == 0, "whole uint4 of bins per thread");
     const int share = SP_THREADS / a.nc;   // threads with bins; nc is a power of two
     const int b0 = PER * (rank * share + tid);
-    unsigned long long hh[PER] = {0, 0, 0, 0};
+    unsigned long long hh[PER] = {};
     if (tid < share) {
-      uint4 x[SP_MAX_CLUSTER];
 #pragma unroll
-      for (int c = 0; c < SP_MAX_CLUSTER; ++c)   // all loads in flight together
-        if (c < a.nc) x[c] = reinterpret_cast<const uint4 *>(dense::peer(&sh->bins[0], c))[b0 / 4];
+      for (int q = 0; q < PER; q += 4) {
+        uint4 x[SP_MAX_CLUSTER];
 #pragma unroll
-      for (int c = 0; c < SP_MAX_CLUSTER; ++c)
-        if (c < a.nc) {
-          hh[0] += x[c].x;
-          hh[1] += x[c].y;
-          hh[2] += x[c].z;
-          hh[3] += x[c].w;
-        }
+        for (int c = 0; c < SP_MAX_CLUSTER; ++c)   // all loads in flight together
+          if (c < a.nc) x[c] = reinterpret_cast<const uint4 *>(dense::peer(&sh->bins[0], c))[(b0 + q) / 4];
+#pragma unroll
+        for (int c = 0; c < SP_MAX_CLUSTER; ++c)
+          if (c < a.nc) {
+            hh[q] += x[c].x;
+            hh[q + 1] += x[c].y;
+            hh[q + 2] += x[c].z;
+            hh[q + 3] += x[c].w;
+          }
+      }
     }
     double f[PER], run = 0.0;
 #pragma unroll
@@ -932,6 +955,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
         all += sh->push[5][c].a;
       }
     }
+    if (!k_on) all = 32768.0 * S;   // (what lies below the bins too)
     // top-k: the bin of rank k. top-p: the bins that the histogram's masses,
     // good to 1.3e-4, leave open.
     const double want = k_on ? fmin((double)top_k, all) : (double)fmaxf(top_p, 0.0f) * all;
@@ -1210,16 +1234,19 @@ __device__ void sp_load(const SpSrc<BF16, RES> &src, float *vals, int padded, fl
   const int full = src.n / 4 * 4;
   for (int i0 = 0; i0 < full; i0 += 4 * U * SP_THREADS) {
     float4 q[U];
+    const int at = i0 + 4 * tid;
+    if (src.vec && i0 + 4 * U * SP_THREADS <= full) {
 #pragma unroll
-    for (int c = 0; c < U; ++c) {
-      const int i = i0 + 4 * (c * SP_THREADS + tid);
-      q[c] = i < full ? mem.four(i, full) : make_float4(-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F);
+      for (int c = 0; c < U; ++c) q[c] = mem.all_four(at + 4 * c * SP_THREADS);
+    } else {
+#pragma unroll
+      for (int c = 0; c < U; ++c) q[c] = mem.four(at + 4 * c * SP_THREADS, full);
     }
 #pragma unroll
     for (int c = 0; c < U; ++c) {
-      const int i = i0 + 4 * (c * SP_THREADS + tid);
+      const int i = at + 4 * c * SP_THREADS;
+      mx = fmaxf(fmaxf(mx, fmaxf(q[c].x, q[c].y)), fmaxf(q[c].z, q[c].w));
       if (i < full) {
-        mx = fmaxf(fmaxf(mx, fmaxf(q[c].x, q[c].y)), fmaxf(q[c].z, q[c].w));
         mn = fminf(fminf(mn, fminf(q[c].x, q[c].y)), fminf(q[c].z, q[c].w));
         if (RES) *reinterpret_cast<float4 *>(vals + i) = q[c];
       }
