@@ -181,6 +181,8 @@ __device__ __forceinline__ void touch(const float *p) {
   asm volatile("{ .reg .f32 t; ld.global.nc.f32 t, [%0]; }" ::"l"(p));
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <bool I8>
 __device__ __forceinline__ float ln_acc(float bits, float sa, float sw) {
   if (I8) return __fmul_rn(__fmul_rn(__int2float_rn(__float_as_int(bits)), sa), sw);
@@ -449,6 +451,11 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
         ln_tile(a, i, ta, tb);
         const int n = ta * LN_ROWS + q * 32 + lane, m0 = tb * BT + col0;
         float v[NCH][16];
+        if (n < a.N) {   // on their way while the products run
+          if (I8) touch(a.s_w + n);
+          if (a.bias) touch(a.bias + n);
+        }
+        if (I8 && lane < EPI_COLS && m0 + lane < a.M) touch(a.s_a + m0 + lane);
         for (int sg = 0; sg < segs; ++sg) {
           const int slot = c & 1;
           ok = wait_slot(slot);
@@ -614,6 +621,15 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
       bool have = false;
       if (warp >= LN_W_EPI) {
         have = true;
+        // what the values that end here need, on its way while the products run
+        const int ends = min(BT, a.M - tb * BT) << fs;
+        for (int i = threadIdx.x - 32 * LN_W_EPI; i < ends; i += 32 * N_EPI) {
+          const int m = tb * BT + (i >> fs), n = ta * LN_ROWS + (rank << fs) + (i & (fl - 1));
+          if (n >= a.N) continue;
+          if (I8) touch(a.s_a + m), touch(a.s_w + n);
+          if (a.bias) touch(a.bias + n);
+          if (a.res) prefetch_l2(static_cast<const uint8_t *>(a.res) + ((long long)m * a.ldr + n) * (a.out_f32 ? 4 : 2));
+        }
         for (int sg = 0; sg < segs && have; ++sg) {
           const int slot = sg & 1;
           have = ln_wait_warp(&b->acc_full[slot], (sg >> 1) & 1, b, a.status);
