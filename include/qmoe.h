@@ -446,8 +446,9 @@ qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, int M, int N
  *          prefix of ranks whose sum of w reaches top_p[t] times their sum
  *   token[t] = the lowest kept index whose running sum of kept w, in index
  *          order, exceeds u[t] times the kept sum;  prob[t] = w / kept sum
- * Sums that decide are float64 in a fixed order: the same inputs give the same
- * token. Masked tokens are -inf (NaN counts as -inf); a row without any
+ * Every choice is checked to lie further from its border than the error of the
+ * sums behind it, or made again from float64 sums in a fixed order: the same
+ * inputs give the same token. Masked tokens are -inf (NaN counts as -inf); a row without any
  * candidate gives token -1 and prob 0. temperature 0 takes the largest logit
  * (the lowest index of equals) with prob 1.
  * temperature, top_p, min_p, u fp32 [T]; top_k int32 [T]; token int32 [T];
