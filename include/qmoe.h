@@ -400,8 +400,8 @@ qmoe_status qmoe_ngram_gather(const int32_t *ngrams, int T, uint64_t seed, const
  * norm_out bf16 [T,H]; codes int8 [T,H]. y, gain, z_out, norm_out may be NULL,
  * and codes with scales; codes or norm_out must be there. z_out may alias x_in
  * or y; no other outputs may alias inputs.
- * Limits: H a multiple of 16 (and of group) up to 16,384, T >= 1. Alignment 16
- * bytes, scales 4. Errors: INVALID_ARG, UNSUPPORTED (H, group). */
+ * Limits: H a multiple of 16 (and of group) up to 16,384, 1 <= T <= 2^30. Alignment
+ * 16 bytes, scales 4. Errors: INVALID_ARG, UNSUPPORTED (H, T, group). */
 qmoe_status qmoe_rmsnorm_residual_q8(const void *x_in, const void *y, int dtype, const float *gain, float eps,
                                      int T, int H, int group, void *z_out, void *norm_out, int8_t *codes,
                                      float *scales, qmoe_stream_t stream);
@@ -426,11 +426,11 @@ qmoe_status qmoe_quantise_rows(const void *x, int dtype, int T, int H, int group
  *   lda, ldw, ldr, ldo: row strides in elements, 0 = packed (K, K, N, N).
  *     Columns past K (or N) of a row are neither read nor written.
  * The result does not depend on timing: sums are formed in a fixed order.
- * Limits: M, N >= 1, 1 <= K <= 65,536; rows of a and w must start on 16 bytes
+ * Limits: 1 <= M, N <= 2^30, 1 <= K <= 65,536; rows of a and w must start on 16 bytes
  * (lda, ldw multiples of 8 for bf16, of 16 for int8). Alignment: 16 bytes.
  * out must not overlap a, w, the scales or bias. Errors: INVALID_ARG (null or
  * misaligned pointers, strides below the row, scales missing or not wanted),
- * UNSUPPORTED (K, row alignment); device status TIMEOUT if a wait inside the
+ * UNSUPPORTED (M, N, K, row alignment); device status TIMEOUT if a wait inside the
  * kernel ran out of its budget. */
 qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, int M, int N, int K, const float *a_scale,
                         const float *w_scale, const float *bias, int act, const void *residual, void *out,
@@ -454,8 +454,8 @@ qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, int M, int N
  * temperature, top_p, min_p, u fp32 [T]; top_k int32 [T]; token int32 [T];
  * prob fp32 [T] or NULL. A NULL temperature is 1; a NULL filter is off, and so
  * are top_k <= 0 or >= V, top_p >= 1 and min_p <= 0. top_p <= 0 keeps one rank.
- * Limits: T >= 1, 1 <= V <= 393,216. Alignment: logits 16 bytes (rows may start
- * anywhere), the others 4. Errors: INVALID_ARG, UNSUPPORTED (V). A row whose
+ * Limits: 1 <= T <= 2^27, 1 <= V <= 393,216. Alignment: logits 16 bytes (rows may start
+ * anywhere), the others 4. Errors: INVALID_ARG, UNSUPPORTED (V, T). A row whose
  * temperature is negative, NaN or infinite, top_p NaN, min_p NaN or above 1, or
  * u outside [0, 1) gets token -1, prob 0 and sets the device status, which
  * qmoe_read_status reports as INVALID_ARG; the other rows are sampled. */

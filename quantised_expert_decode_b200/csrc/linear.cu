@@ -46,6 +46,7 @@ constexpr int LN_W_TMA = 0, LN_W_MMA = 1, LN_W_EPI = 2;
 constexpr int LN_MAX_STAGES = 10;
 constexpr int LN_MAX_SPLIT = 8;
 constexpr int LN_MAX_K = 65536;                  // keeps |int32 sums| below 2^31
+constexpr int LN_MAX_MN = 1 << 30;               // tile ends stay below 2^31
 constexpr int LN_SMEM = 224 * 1024;              // ring and staging
 constexpr int LN_BOX = 4096;                     // staging: 32 rows of 128 bytes
 constexpr int LN_GROUP = 8;                      // A tiles that share B tiles in L2
@@ -778,7 +779,7 @@ extern "C" qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, i
       !aligned16(w_scale) || !aligned16(bias) || (reinterpret_cast<uintptr_t>(dev_status) & 3))
     return QMOE_ERR_INVALID_ARG;
   // rows of a and w start on 16 bytes (the copy engine's rule); strides below 2^40 bytes
-  if (lda * es % 16 || ldw * es % 16 || K > LN_MAX_K || lda > (1LL << 38) || ldw > (1LL << 38)) return QMOE_ERR_UNSUPPORTED;
+  if (lda * es % 16 || ldw * es % 16 || K > LN_MAX_K || M > LN_MAX_MN || N > LN_MAX_MN || lda > (1LL << 38) || ldw > (1LL << 38)) return QMOE_ERR_UNSUPPORTED;
   LnArgs g{};
   g.s_a = a_scale;
   g.s_w = w_scale;

@@ -30,7 +30,7 @@ namespace {
 
 constexpr int NQ_VEC = 8;                    // columns per thread and chunk: 16 bytes of bf16, 8 bytes of codes
 constexpr int NQ_MAX_THREADS = 512;
-constexpr int NQ_MAX_H = 16384;
+constexpr int NQ_MAX_H = 16384, NQ_MAX_T = 1 << 30;
 constexpr float NQ_MAGIC = 12582912.0f;      // 1.5 * 2^23: adding it rounds to an integer, ties to even
 constexpr float NQ_ERR = 3.1e-7f;            // bound of a code's fp32 error relative to it: five roundings of 2^-24
 // fp32 statistics outside these are formed again in float64
@@ -431,7 +431,7 @@ extern "C" qmoe_status qmoe_rmsnorm_residual_q8(const void *x_in, const void *y,
       !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3))
     return QMOE_ERR_INVALID_ARG;
   if (!(eps >= 0.0f)) return QMOE_ERR_INVALID_ARG;
-  if (H % 16 || H > NQ_MAX_H || !nq_group_ok(group, H)) return QMOE_ERR_UNSUPPORTED;
+  if (T > NQ_MAX_T || H % 16 || H > NQ_MAX_H || !nq_group_ok(group, H)) return QMOE_ERR_UNSUPPORTED;
   NqArgs a{x_in, y, gain, z_out, static_cast<__nv_bfloat16 *>(norm_out), codes, scales, eps, T, H, group};
   return nq_launch(a, dtype, true, (cudaStream_t)stream);
 }
@@ -441,7 +441,7 @@ extern "C" qmoe_status qmoe_quantise_rows(const void *x, int dtype, int T, int H
   if (!x || !codes || !scales || T < 1 || H < 1 || (dtype != QMOE_F32 && dtype != QMOE_BF16))
     return QMOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 3)) return QMOE_ERR_INVALID_ARG;
-  if (H % 16 || H > NQ_MAX_H || !nq_group_ok(group, H)) return QMOE_ERR_UNSUPPORTED;
+  if (T > NQ_MAX_T || H % 16 || H > NQ_MAX_H || !nq_group_ok(group, H)) return QMOE_ERR_UNSUPPORTED;
   NqArgs a{x, nullptr, nullptr, nullptr, nullptr, codes, scales, 0.0f, T, H, group};
   return nq_launch(a, dtype, false, (cudaStream_t)stream);
 }

@@ -17,7 +17,7 @@
 // row by as many of them as there are to spare.
 // Bound: for few rows the chain of its steps (some ten cluster barriers and as
 // many short sums of a few hundred cycles each: 1 x 131072 with top-k, top-p and
-// min-p 16 us, 8 x 131072 bf16 with top-p 33 us); for many the issue of some 65
+// min-p 16.6 us, 8 x 131072 bf16 with top-p 34 us); for many the issue of some 65
 // instructions per logit (256 x 131072 fp32 with top-p 137 us, 15 % of the
 // measured copy rate).
 //
@@ -54,13 +54,13 @@ constexpr int SP_BINS = 1024;                 // exact way
 constexpr int SQ_BINS = 2048;                 // quick way: 11 bits of bin, 12 bits of place within it (4096 bins: 6 % slower)
 constexpr int SQ_SUB = 12;
 constexpr int SQ_ROUND = 256;                 // logits of a warp whose sums are kept apart: two float4 per lane
-constexpr int SQ_LIST = 1024;                 // elements that the quick way gathers and sorts
+constexpr int SQ_LIST = 2048;                 // elements that the quick way gathers and sorts
 constexpr double SP_EPS = 1e-11;              // bound of the quick sums' error, relative to the row's sum
 constexpr int SP_LIST = 512;                  // elements ranked one by one (one per thread)
 constexpr int SP_MAX_CLUSTER = 8;             // CTAs per row
 constexpr long long SP_L2_BYTES = 126ll << 20;
 constexpr int SP_MAX_SLICE = 32768;           // 128 KB of fp32 logits per CTA
-constexpr int SP_MAX_V = 393216;
+constexpr int SP_MAX_V = 393216, SP_MAX_T = 1 << 27;
 constexpr double SP_W_MIN = 5.421010862427522e-20;   // 2^-64
 constexpr int SP_FIX = 44;                    // histogram masses in units of 2^-44
 constexpr float SP_LOWEST = -3.402823466e38f;
@@ -598,8 +598,8 @@ __device__ __forceinline__ unsigned long long sq_key(float l, int i) {
 }
 __device__ __forceinline__ float sq_key_logit(unsigned long long k) { return key_float(~(unsigned)(k >> 32)); }
 
-// Sorts the n keys, ascending (all threads of the CTA; a bitonic network, one
-// pair per thread).
+// Sorts the n keys, ascending (all threads of the CTA; a bitonic network, a pair
+// per thread and turn).
 __device__ void sq_sort(SpShared *sh, int n) {
   const int tid = threadIdx.x;
   int size = 2;
@@ -608,8 +608,8 @@ __device__ void sq_sort(SpShared *sh, int n) {
   __syncthreads();
   for (int k = 2; k <= size; k *= 2)
     for (int j = k / 2; j > 0; j /= 2) {
-      if (tid < size / 2) {
-        const int a = 2 * tid - (tid & (j - 1)), b = a + j;
+      for (int p = tid; p < size / 2; p += SP_THREADS) {
+        const int a = 2 * p - (p & (j - 1)), b = a + j;
         const unsigned long long x = sh->keys[a], y = sh->keys[b];
         if ((x > y) == ((a & k) == 0)) {
           sh->keys[a] = y;
@@ -617,7 +617,7 @@ __device__ void sq_sort(SpShared *sh, int n) {
         }
       }
       if (j > 32) __syncthreads();
-      else __syncwarp();   // up to there a warp's pairs stay within its own 64 keys
+      else __syncwarp();   // up to there a warp's pairs stay within its own 64 keys (of each turn)
       if (j == 1) __syncthreads();
     }
 }
@@ -1444,7 +1444,7 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
                        reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(token) |
                        reinterpret_cast<uintptr_t>(prob) | reinterpret_cast<uintptr_t>(dev_status);
   if ((a4 & 3) || !aligned16(logits)) return QMOE_ERR_INVALID_ARG;
-  if (V > SP_MAX_V || T > (1 << 27)) return QMOE_ERR_UNSUPPORTED;
+  if (V > SP_MAX_V || T > SP_MAX_T) return QMOE_ERR_UNSUPPORTED;
   const auto smem_of = [](bool res, int seg) { return (int)(sp_head_bytes() + (size_t)SP_WARPS * (SQ_ROUND + (res ? seg : 0)) * 4); };
   const auto kernel = [&](bool res) {
     return dtype == QMOE_BF16 ? (res ? (const void *)sample_kernel<true, true> : (const void *)sample_kernel<true, false>)

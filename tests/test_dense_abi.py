@@ -72,6 +72,15 @@ def test_sample_argument_checks():
     assert call(V=393217) == 3
 
 
+def test_sizes_past_the_limits_are_refused():
+    lib, F = q.lib(), FAKE
+    assert lib.qmoe_rmsnorm_residual_q8(F, None, q.F32, None, ctypes.c_float(0), (1 << 30) + 1, 16, 0, None, None, F, F, None) == 3
+    assert lib.qmoe_quantise_rows(F, q.F32, (1 << 30) + 1, 16, 0, F, F, None) == 3
+    for M, N in (((1 << 30) + 1, 1), (1, (1 << 30) + 1)):
+        assert lib.qmoe_linear(F, q.BF16, F, M, N, 8, None, None, None, 0, None, F, q.F32, 0, 0, 0, 0, F, None) == 3
+    assert lib.qmoe_sample(F, q.F32, (1 << 27) + 1, 1, 0, None, None, None, None, F, F, None, F, None) == 3
+
+
 class _OnAnotherDevice:
     """Just enough of a tensor to be looked at."""
 
