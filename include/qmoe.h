@@ -430,7 +430,7 @@ qmoe_status qmoe_quantise_rows(const void *x, int dtype, int T, int H, int group
  * (lda, ldw multiples of 8 for bf16, of 16 for int8). Alignment: 16 bytes.
  * out must not overlap a, w, the scales or bias. Errors: INVALID_ARG (null or
  * misaligned pointers, strides below the row, scales missing or not wanted),
- * UNSUPPORTED (M, N, K, row alignment); device status TIMEOUT if a wait inside the
+ * UNSUPPORTED (M, N, K, row alignment, strides above 2^37); device status TIMEOUT if a wait inside the
  * kernel ran out of its budget. */
 qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, int M, int N, int K, const float *a_scale,
                         const float *w_scale, const float *bias, int act, const void *residual, void *out,

@@ -262,7 +262,7 @@ def qmoe_linear(a, in_dtype, w, M, N, K, a_scale, w_scale, bias, act, residual, 
     dt, odt = _DTYPES.get(in_dtype, "bfloat16"), _DTYPES.get(out_dtype, "float32")
     _fits("qmoe_linear", (a, dt, M, K, lda or K), (w, dt, N, K, ldw or K), (a_scale, "float32", 1, M, 0),
           (w_scale, "float32", 1, N, 0), (bias, "float32", 1, N, 0), (residual, odt, M, N, ldr or N),
-          (out, odt, M, N, ldo or N))
+          (out, odt, M, N, ldo or N), (dev_status, "int32", 1, 1, 0))
     _check("qmoe_linear", lib().qmoe_linear(
         _p(a), in_dtype, _p(w), M, N, K, _p(a_scale), _p(w_scale), _p(bias), act, _p(residual), _p(out), out_dtype,
         lda, ldw, ldr, ldo, _p(dev_status), _s(stream)))
@@ -274,7 +274,7 @@ def qmoe_sample(logits, dtype, T, V, temperature, top_k, top_p, min_p, u, token,
     fp32 [T] or None, ``top_k`` int32 [T] or None, ``u`` fp32 [T]; ``token`` int32 [T], ``prob`` fp32 [T] or None."""
     _fits("qmoe_sample", (logits, _DTYPES.get(dtype, "float32"), T, V, ld or V), (temperature, "float32", 1, T, 0),
           (top_k, "int32", 1, T, 0), (top_p, "float32", 1, T, 0), (min_p, "float32", 1, T, 0), (u, "float32", 1, T, 0),
-          (token, "int32", 1, T, 0), (prob, "float32", 1, T, 0))
+          (token, "int32", 1, T, 0), (prob, "float32", 1, T, 0), (dev_status, "int32", 1, 1, 0))
     _check("qmoe_sample", lib().qmoe_sample(_p(logits), dtype, T, V, ld, _p(temperature), _p(top_k), _p(top_p),
                                             _p(min_p), _p(u), _p(token), _p(prob), _p(dev_status), _s(stream)))
 

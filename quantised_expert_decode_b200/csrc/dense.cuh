@@ -21,6 +21,13 @@ namespace dense {
 constexpr int MAX_CLUSTER = 8;
 int max_clusters(int size, const void *fn, int threads, int smem);
 
+// The status of a call that launched nothing more: a refused launch leaves no error
+// behind that a later call would take for its own.
+inline qmoe_status launched(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return cuda_status(e);
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void *p = nullptr;

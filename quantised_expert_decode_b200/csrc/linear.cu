@@ -47,6 +47,7 @@ constexpr int LN_MAX_STAGES = 10;
 constexpr int LN_MAX_SPLIT = 8;
 constexpr int LN_MAX_K = 65536;                  // keeps |int32 sums| below 2^31
 constexpr int LN_MAX_MN = 1 << 30;               // tile ends stay below 2^31
+constexpr long long LN_MAX_LD = 1LL << 37;       // elements: below the tensor maps' 2^40 bytes
 constexpr int LN_SMEM = 224 * 1024;              // ring and staging
 constexpr int LN_BOX = 4096;                     // staging: 32 rows of 128 bytes
 constexpr int LN_GROUP = 8;                      // A tiles that share B tiles in L2
@@ -735,7 +736,8 @@ int ln_max_clusters(int size) {
 }
 
 qmoe_status ln_launch(const void *fn, int smem, int threads, const LnArgs &a, int grid, int cluster, cudaStream_t s) {
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return QMOE_ERR_CUDA;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return dense::launched(e);
   LnArgs args = a;
   void *params[] = {&args};
   cudaLaunchConfig_t cfg{};
@@ -749,9 +751,9 @@ qmoe_status ln_launch(const void *fn, int smem, int threads, const LnArgs &a, in
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, params);
+  e = cudaLaunchKernelExC(&cfg, fn, params);
   note_launch();
-  return cuda_status(e);
+  return dense::launched(e);
 }
 
 }  // namespace
@@ -779,7 +781,8 @@ extern "C" qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, i
       !aligned16(w_scale) || !aligned16(bias) || (reinterpret_cast<uintptr_t>(dev_status) & 3))
     return QMOE_ERR_INVALID_ARG;
   // rows of a and w start on 16 bytes (the copy engine's rule); strides below 2^40 bytes
-  if (lda * es % 16 || ldw * es % 16 || K > LN_MAX_K || M > LN_MAX_MN || N > LN_MAX_MN || lda > (1LL << 38) || ldw > (1LL << 38)) return QMOE_ERR_UNSUPPORTED;
+  if (lda > LN_MAX_LD || ldw > LN_MAX_LD || ldo > LN_MAX_LD || (residual && ldr > LN_MAX_LD)) return QMOE_ERR_UNSUPPORTED;
+  if (lda * es % 16 || ldw * es % 16 || K > LN_MAX_K || M > LN_MAX_MN || N > LN_MAX_MN) return QMOE_ERR_UNSUPPORTED;
   LnArgs g{};
   g.s_a = a_scale;
   g.s_w = w_scale;

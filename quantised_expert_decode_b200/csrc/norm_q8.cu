@@ -23,7 +23,7 @@
 // from every row (a third of the speed).
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "dense.cuh"
 
 namespace qmoe {
 namespace {
@@ -403,16 +403,16 @@ qmoe_status nq_launch(const NqArgs &a, int dtype, bool norm, cudaStream_t s) {
   const void *fn = norm ? (dtype == QMOE_BF16 ? (const void *)norm_q8_kernel<true, true> : (const void *)norm_q8_kernel<false, true>)
                         : (dtype == QMOE_BF16 ? (const void *)norm_q8_kernel<true, false> : (const void *)norm_q8_kernel<false, false>);
   const size_t smem = 2 * (size_t)a.H * sizeof(float);
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return QMOE_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return dense::launched(e);
   const long long cap = 1024LL / threads * sms;
   const int grid = a.T < cap ? a.T : (int)cap;
   NqArgs args = a;
   void *params[] = {&args};
-  const cudaError_t e = cudaLaunchKernel(fn, dim3(grid), dim3(threads), params, smem, s);
+  e = cudaLaunchKernel(fn, dim3(grid), dim3(threads), params, smem, s);
   note_launch();
-  return cuda_status(e);
+  return dense::launched(e);
 }
 
 bool nq_group_ok(int group, int H) { return group == 0 || ((group == 32 || group == 64 || group == 128) && H % group == 0); }

@@ -1470,8 +1470,8 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   const int smem = smem_of(res, seg);
   SpArgs args{logits, temperature, top_p, min_p, u, top_k, token, prob, dev_status, ld, T, V, slice, nc, seg, (seg + SQ_ROUND - 1) / SQ_ROUND};
   const void *fn = kernel(res);
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return QMOE_ERR_CUDA;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return dense::launched(e);
   void *params[] = {&args};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)T * (unsigned)nc);
@@ -1484,7 +1484,7 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, params);
+  e = cudaLaunchKernelExC(&cfg, fn, params);
   note_launch();
-  return cuda_status(e);
+  return dense::launched(e);
 }

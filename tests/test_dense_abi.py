@@ -81,6 +81,31 @@ def test_sizes_past_the_limits_are_refused():
     assert lib.qmoe_sample(F, q.F32, (1 << 27) + 1, 1, 0, None, None, None, None, F, F, None, F, None) == 3
 
 
+def test_linear_strides_past_the_limit_are_refused():
+    lib, F, big = q.lib(), FAKE, 1 << 62
+
+    def call(lda=0, ldw=0, ldr=0, ldo=0):
+        return lib.qmoe_linear(F, q.BF16, F, 2, 8, 8, None, None, None, 0, F, F, q.F32, lda, ldw, ldr, ldo, F, None)
+
+    for name in ("lda", "ldw", "ldr", "ldo"):
+        assert call(**{name: big}) == 3 and call(**{name: (1 << 37) + 8}) == 3, name
+
+
+@pytest.mark.gpu
+def test_binding_refuses_a_status_word_off_the_device():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("needs a device to be off of")
+    st = torch.zeros(1, dtype=torch.int32)
+    x = torch.zeros((1, 64), device="cuda")
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(q.QmoeError):
+        q.qmoe_sample(x, q.F32, 1, 64, None, None, None, None, x[0, :1], i, None, st)
+    b = torch.zeros((1, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(q.QmoeError):
+        q.qmoe_linear(b, q.BF16, b, 1, 1, 64, None, None, None, 0, None, x, q.F32, st)
+
+
 class _OnAnotherDevice:
     """Just enough of a tensor to be looked at."""
 
