@@ -206,23 +206,31 @@ def qmoe_ngram_gather(ngrams, T, seed, codes, scales, R, D, out, rows=None, stre
                                                         R, D, _p(out), _p(rows), _s(stream)))
 
 
+_TORCH_TYPES: dict = {}
 _DTYPES = {F32: "float32", BF16: "bfloat16", I8: "int8"}
 
 
-def _fits(fn: str, *wants) -> None:
+def _fits(fn: str, *wants) -> list:
     """(tensor or None, type, rows, columns, row stride) each: on the current device, of the type, rows dense,
-    and large enough for what the call reads or writes. A plain address (int) is the caller's word."""
+    and large enough for what the call reads or writes. A plain address (int) is the caller's word. Returns
+    their addresses (one pass over the tensors: a short kernel takes less time than asking them twice)."""
     import torch
-    dev = torch.cuda.current_device()
+    if not _TORCH_TYPES:
+        _TORCH_TYPES.update((name, getattr(torch, name)) for name in ("float32", "bfloat16", "int8", "int32"))
+    dev, tensor, types, out = torch.cuda.current_device(), torch.Tensor, _TORCH_TYPES, []
     for t, dtype, rows, cols, ld in wants:
-        if t is None or isinstance(t, int):
+        if t is None:
+            out.append(None)
             continue
         # a packed tensor of its own rows, as most are, with few questions to it; the others one by one
-        if t.dtype is getattr(torch, dtype) and t.get_device() == dev and t.is_contiguous():
-            shape = t.shape
-            if (ld == cols or not ld) and t.numel() >= rows * cols and (len(shape) < 2 or not ld or shape[-1] == ld):
-                continue
-        if t.dtype != getattr(torch, dtype):
+        if (type(t) is tensor and t.dtype is types[dtype] and t.get_device() == dev and t.is_contiguous()
+                and t.numel() >= rows * cols and (not ld or (ld == cols and (t.dim() < 2 or t.size(-1) == ld)))):
+            out.append(t.data_ptr())
+            continue
+        if isinstance(t, int):
+            out.append(t)
+            continue
+        if t.dtype != types[dtype]:
             raise QmoeError(fn + f" (a {t.dtype} tensor in the place of a {dtype} one)", 1)
         if t.get_device() != dev:
             raise QmoeError(fn + " (a tensor on another device than the current one)", 1)
@@ -232,6 +240,8 @@ def _fits(fn: str, *wants) -> None:
             raise QmoeError(fn + " (a tensor whose row stride is not the one given)", 1)
         if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < (rows - 1) * (ld or cols) + cols:
             raise QmoeError(fn + " (a tensor smaller than the call's sizes)", 1)
+        out.append(t.data_ptr())
+    return out
 
 
 def qmoe_rmsnorm_residual_q8(x_in, y, dtype, gain, eps, T, H, group, z_out, norm_out, codes, scales, stream=None) -> None:
@@ -239,19 +249,19 @@ def qmoe_rmsnorm_residual_q8(x_in, y, dtype, gain, eps, T, H, group, z_out, norm
     ``codes`` int8 [T, H]; ``scales`` fp32 [T] (``group`` 0) or [T, H / group]. Any of y, gain, z_out, norm_out
     and (codes, scales) may be None."""
     dt = _DTYPES.get(dtype, "float32")
-    _fits("qmoe_rmsnorm_residual_q8", (x_in, dt, T, H, H), (y, dt, T, H, H), (gain, "float32", 1, H, 0),
-          (z_out, dt, T, H, H), (norm_out, "bfloat16", T, H, H), (codes, "int8", T, H, H),
-          (scales, "float32", 1, T * (H // group if group > 0 else 1), 0))
-    _check("qmoe_rmsnorm_residual_q8", lib().qmoe_rmsnorm_residual_q8(
-        _p(x_in), _p(y), dtype, _p(gain), float(eps), T, H, group, _p(z_out), _p(norm_out), _p(codes), _p(scales),
-        _s(stream)))
+    x, y, g, z, n, c, s = _fits(
+        "qmoe_rmsnorm_residual_q8", (x_in, dt, T, H, H), (y, dt, T, H, H), (gain, "float32", 1, H, 0),
+        (z_out, dt, T, H, H), (norm_out, "bfloat16", T, H, H), (codes, "int8", T, H, H),
+        (scales, "float32", 1, T * (H // group if group > 0 else 1), 0))
+    _check("qmoe_rmsnorm_residual_q8", lib().qmoe_rmsnorm_residual_q8(x, y, dtype, g, eps, T, H, group, z, n, c, s,
+                                                                      _s(stream)))
 
 
 def qmoe_quantise_rows(x, dtype, T, H, group, codes, scales, stream=None) -> None:
     """``x`` fp32 or bf16 [T, H] -> ``codes`` int8 [T, H] and ``scales`` fp32 [T] or [T, H / group]."""
-    _fits("qmoe_quantise_rows", (x, _DTYPES.get(dtype, "float32"), T, H, H), (codes, "int8", T, H, H),
-          (scales, "float32", 1, T * (H // group if group > 0 else 1), 0))
-    _check("qmoe_quantise_rows", lib().qmoe_quantise_rows(_p(x), dtype, T, H, group, _p(codes), _p(scales), _s(stream)))
+    x, c, s = _fits("qmoe_quantise_rows", (x, _DTYPES.get(dtype, "float32"), T, H, H), (codes, "int8", T, H, H),
+                    (scales, "float32", 1, T * (H // group if group > 0 else 1), 0))
+    _check("qmoe_quantise_rows", lib().qmoe_quantise_rows(x, dtype, T, H, group, c, s, _s(stream)))
 
 
 def qmoe_linear(a, in_dtype, w, M, N, K, a_scale, w_scale, bias, act, residual, out, out_dtype, dev_status, lda=0,
@@ -260,23 +270,23 @@ def qmoe_linear(a, in_dtype, w, M, N, K, a_scale, w_scale, bias, act, residual, 
     with ``a_scale`` fp32 [M] and ``w_scale`` fp32 [N] (I8); ``bias`` fp32 [N] or None; ``residual`` and ``out``
     [M, N] of ``out_dtype``; strides in elements, 0 = packed."""
     dt, odt = _DTYPES.get(in_dtype, "bfloat16"), _DTYPES.get(out_dtype, "float32")
-    _fits("qmoe_linear", (a, dt, M, K, lda or K), (w, dt, N, K, ldw or K), (a_scale, "float32", 1, M, 0),
-          (w_scale, "float32", 1, N, 0), (bias, "float32", 1, N, 0), (residual, odt, M, N, ldr or N),
-          (out, odt, M, N, ldo or N), (dev_status, "int32", 1, 1, 0))
-    _check("qmoe_linear", lib().qmoe_linear(
-        _p(a), in_dtype, _p(w), M, N, K, _p(a_scale), _p(w_scale), _p(bias), act, _p(residual), _p(out), out_dtype,
-        lda, ldw, ldr, ldo, _p(dev_status), _s(stream)))
+    a, w, sa, sw, b, r, o, st = _fits(
+        "qmoe_linear", (a, dt, M, K, lda or K), (w, dt, N, K, ldw or K), (a_scale, "float32", 1, M, 0),
+        (w_scale, "float32", 1, N, 0), (bias, "float32", 1, N, 0), (residual, odt, M, N, ldr or N),
+        (out, odt, M, N, ldo or N), (dev_status, "int32", 1, 1, 0))
+    _check("qmoe_linear", lib().qmoe_linear(a, in_dtype, w, M, N, K, sa, sw, b, act, r, o, out_dtype, lda, ldw, ldr, ldo,
+                                            st, _s(stream)))
 
 
 def qmoe_sample(logits, dtype, T, V, temperature, top_k, top_p, min_p, u, token, prob, dev_status, ld=0,
                 stream=None) -> None:
     """``logits`` fp32 or bf16 [T, V] (row stride ``ld`` elements, 0 = V); ``temperature``, ``top_p``, ``min_p``
     fp32 [T] or None, ``top_k`` int32 [T] or None, ``u`` fp32 [T]; ``token`` int32 [T], ``prob`` fp32 [T] or None."""
-    _fits("qmoe_sample", (logits, _DTYPES.get(dtype, "float32"), T, V, ld or V), (temperature, "float32", 1, T, 0),
-          (top_k, "int32", 1, T, 0), (top_p, "float32", 1, T, 0), (min_p, "float32", 1, T, 0), (u, "float32", 1, T, 0),
-          (token, "int32", 1, T, 0), (prob, "float32", 1, T, 0), (dev_status, "int32", 1, 1, 0))
-    _check("qmoe_sample", lib().qmoe_sample(_p(logits), dtype, T, V, ld, _p(temperature), _p(top_k), _p(top_p),
-                                            _p(min_p), _p(u), _p(token), _p(prob), _p(dev_status), _s(stream)))
+    x, t, k, p, m, u, tok, pr, st = _fits(
+        "qmoe_sample", (logits, _DTYPES.get(dtype, "float32"), T, V, ld or V), (temperature, "float32", 1, T, 0),
+        (top_k, "int32", 1, T, 0), (top_p, "float32", 1, T, 0), (min_p, "float32", 1, T, 0), (u, "float32", 1, T, 0),
+        (token, "int32", 1, T, 0), (prob, "float32", 1, T, 0), (dev_status, "int32", 1, 1, 0))
+    _check("qmoe_sample", lib().qmoe_sample(x, dtype, T, V, ld, t, k, p, m, u, tok, pr, st, _s(stream)))
 
 
 PREFILL_ATOMIC_COMBINE = 1
