@@ -28,6 +28,27 @@ inline qmoe_status launched(cudaError_t e) {
   return cuda_status(e);
 }
 
+// Launches `fn` in clusters of `cluster` CTAs behind the stream's last kernel, set up while
+// that one still runs: the kernel waits (pdl_wait) before it touches global memory.
+inline qmoe_status launch(const void *fn, int grid, int threads, int smem, int cluster, void **params, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, params);
+  note_launch();
+  return launched(e);
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void *p = nullptr;

@@ -328,6 +328,8 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
   if (PAIRS) dense::cluster_sync();   // the other CTA's barriers are ready
   else if (a.split > 1) dense::cluster_arrive();   // (waited for before the CTAs exchange sums)
   tc05::fence_after_sync();
+  pdl_wait();   // (so far nothing but this kernel's own memory)
+  pdl_launch_dependents();
   const uint32_t tmem = b->tmem_base;
   const int ntiles = a.tiles_a * a.tiles_b;
   const int per = PAIRS ? 2 : a.split;   // CTAs that share a tile
@@ -736,24 +738,11 @@ int ln_max_clusters(int size) {
 }
 
 qmoe_status ln_launch(const void *fn, int smem, int threads, const LnArgs &a, int grid, int cluster, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return dense::launched(e);
   LnArgs args = a;
   void *params[] = {&args};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelExC(&cfg, fn, params);
-  note_launch();
-  return dense::launched(e);
+  return dense::launch(fn, grid, threads, smem, cluster, params, s);
 }
 
 }  // namespace

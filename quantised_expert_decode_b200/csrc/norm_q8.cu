@@ -14,8 +14,8 @@
 //
 // Bound: HBM bandwidth for fp32 rows (one read of x and y, one write per output; z
 // waits in shared memory between the statistics and the codes: 8192 x 2048 with
-// x, y and z in fp32 41.6 us, 80 % of the measured copy rate), for bf16 rows the
-// issue of some 40 instructions a column (8192 x 2048 with the normed rows too 33.6 us,
+// x, y and z in fp32 41.1 us, 81 % of the measured copy rate), for bf16 rows the
+// issue of some 40 instructions a column (8192 x 2048 with the normed rows too 33.5 us,
 // 69 %). One CTA per row at a time, 8 neighbouring columns per thread and round, CTAs
 // loop over rows, two rows' z in turn, so that one CTA barrier per row carries all
 // statistics; the next row is fetched into L2 meanwhile. What is rare follows the
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(NQ_MAX_THREADS, 2) norm_q8_kernel(const __grid
   const int gl = a.group / NQ_VEC;   // lanes per group
   const float inv_h = 1.0f / (float)a.H;
 
+  pdl_wait();   // (the next kernel is let in at the end only: its waiting CTAs took places unevenly, 4 % at 1003 x 5248)
   int par = 0;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x, par ^= 1) {
     const size_t row = (size_t)t * a.H;
@@ -410,9 +411,7 @@ qmoe_status nq_launch(const NqArgs &a, int dtype, bool norm, cudaStream_t s) {
   const int grid = a.T < cap ? a.T : (int)cap;
   NqArgs args = a;
   void *params[] = {&args};
-  e = cudaLaunchKernel(fn, dim3(grid), dim3(threads), params, smem, s);
-  note_launch();
-  return dense::launched(e);
+  return dense::launch(fn, grid, threads, (int)smem, 1, params, s);
 }
 
 bool nq_group_ok(int group, int H) { return group == 0 || ((group == 32 || group == 64 || group == 128) && H % group == 0); }

@@ -17,8 +17,8 @@
 // row by as many of them as there are to spare.
 // Bound: for few rows the chain of its steps (some ten cluster barriers and as
 // many short sums of a few hundred cycles each: 1 x 131072 with top-k, top-p and
-// min-p 16.6 us, 8 x 131072 bf16 with top-p 34 us); for many the issue of some 65
-// instructions per logit (256 x 131072 fp32 with top-p 137 us, 15 % of the
+// min-p 16.4 us, 8 x 131072 bf16 with top-p 33 us); for many the issue of some 65
+// instructions per logit (256 x 131072 fp32 with top-p 136 us, 15 % of the
 // measured copy rate).
 //
 // How the border is found:
@@ -587,9 +587,11 @@ __device__ __forceinline__ void sq_stack(uint32_t &at, float l, float hi) {
                : "+r"(at) : "f"(l), "f"(hi) : "memory");
 }
 
+// By one whole warp with the same v in all lanes: a lane per CTA.
 template <typename T>
 __device__ __forceinline__ void push_all(T *at, const T &v, int nc) {
-  for (int c = 0; c < nc; ++c) *dense::peer(at, c) = v;
+  const int lane = threadIdx.x & 31;
+  if (lane < nc) *dense::peer(at, lane) = v;
 }
 
 // Ascending keys are ascending ranks: logit descending, then index.
@@ -741,7 +743,7 @@ __device__ int sq_collect(SpShared *sh, const SpPush *push, const SpArgs &a, int
 template <bool BF16, bool RES>
 __device__ bool sq_finish_k(const SpSrc<BF16, RES> &src, int s0, int own, int base, float from, int top_k, float top_p, float u,
                             const SqRow &r, SpShared *sh, const SpArgs &a, int t, int rank) {
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   sq_each(src, s0, own, [&](int i, const float(&l)[8]) {
     unsigned in = 0;
 #pragma unroll
@@ -749,7 +751,7 @@ __device__ bool sq_finish_k(const SpSrc<BF16, RES> &src, int s0, int own, int ba
     sq_gather(src, sh, s0 + i, in, base);
   });
   __syncthreads();
-  if (tid == 0) push_all(&sh->push[1][rank], SpPush{0.0, 0.0, 0.0f, 0, (int)sh->list_n, 0}, a.nc);
+  if (wid == 0) push_all(&sh->push[1][rank], SpPush{0.0, 0.0, 0.0f, 0, (int)sh->list_n, 0}, a.nc);
   dense::cluster_sync();
   int kept = sq_collect(sh, sh->push[1], a, rank);
   if (rank == 0) {
@@ -804,7 +806,7 @@ __device__ bool sq_finish_k(const SpSrc<BF16, RES> &src, int s0, int own, int ba
         }
       }
     }
-    if (tid == 0) push_all(&sh->push[4][0], SpPush{0.0, 0.0, 0.0f, good ? 0 : 1}, a.nc);
+    if (wid == 0) push_all(&sh->push[4][0], SpPush{0.0, 0.0, 0.0f, good ? 0 : 1}, a.nc);
   }
   dense::cluster_sync();
   return sh->push[4][0].bad == 0;
@@ -893,12 +895,13 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
       s = sq_cta_sum(warp_sum_d(s), sh->warp_d[0]);
       sy = (float)sq_cta_sum((double)warp_sum(sy), sh->warp_d[1]);
     }
+    if (wid == 0) push_all(&sh->push[0][rank], SpPush{s, (double)sy, 0.0f, bad}, a.nc);
     if (tid == 0) {
-      push_all(&sh->push[0][rank], SpPush{s, (double)sy, 0.0f, bad}, a.nc);
       sh->found = sh->last = SQ_BINS;
       sh->list_n = 0;
     }
     dense::cluster_sync();
+#pragma unroll 1
     for (int c = 0; c < a.nc; ++c) {
       S += sh->push[0][c].a;
       SY += sh->push[0][c].b;
@@ -947,9 +950,10 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     sq_cta_scan(__shfl_sync(0xffffffffu, incl, 31), sh->warp_d[1], before, all);
     double pre = __shfl_sync(0xffffffffu, before, wid) + incl - run;
     if (a.nc > 1) {
-      if (tid == 0) push_all(&sh->push[5][rank], SpPush{all, 0.0, 0.0f, 0}, a.nc);
+      if (wid == 0) push_all(&sh->push[5][rank], SpPush{all, 0.0, 0.0f, 0}, a.nc);
       dense::cluster_sync();
       all = 0.0;
+#pragma unroll 1
       for (int c = 0; c < a.nc; ++c) {
         if (c < rank) pre += sh->push[5][c].a;
         all += sh->push[5][c].a;
@@ -1043,9 +1047,10 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     __syncthreads();
     a_sy = (float)sq_cta_sum((double)warp_sum(a_sy), sh->warp_d[1]);
   }
-  if (tid == 0) push_all(&sh->push[1][rank], SpPush{sum, a_fast, a_sy, bad, (int)sh->list_n, 0}, a.nc);
+  if (wid == 0) push_all(&sh->push[1][rank], SpPush{sum, a_fast, a_sy, bad, (int)sh->list_n, 0}, a.nc);
   dense::cluster_sync();
   double total = 0.0;
+#pragma unroll 1
   for (int c = 0; c < a.nc; ++c) {
     total += sh->push[1][c].a;
     S -= sh->push[1][c].b;       // what is left is below the border's bins, or in them
@@ -1116,9 +1121,10 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
         s += sq_weight(l >= hi ? l : -CUDART_INF_F, r, sh->exp2_tab);
       }
       s = sq_cta_sum(warp_sum_d(s), sh->warp_d[1]);
-      if (tid == 0) push_all(&sh->push[2][rank], SpPush{s, 0.0, 0.0f, 0}, a.nc);
+      if (wid == 0) push_all(&sh->push[2][rank], SpPush{s, 0.0, 0.0f, 0}, a.nc);
       dense::cluster_sync();
       whole = 0.0;
+#pragma unroll 1
       for (int c = 0; c < a.nc; ++c) whole += sh->push[2][c].a;
       err = SP_EPS * whole;
     }
@@ -1136,7 +1142,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
     for (int i = lane; i * SQ_ROUND < own; i += 32) ws += sh->rounds[wid * a.rounds + i];
     ws = warp_sum_d(ws);
     sq_cta_scan(ws, sh->warp_d[1], warps_before, sum);
-    if (tid == 0) push_all(&sh->push[3][rank], SpPush{sum, 0.0, 0.0f, 0}, a.nc);
+    if (wid == 0) push_all(&sh->push[3][rank], SpPush{sum, 0.0, 0.0f, 0}, a.nc);
     dense::cluster_sync();
   }
 
@@ -1145,6 +1151,7 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
   const double aim = (double)u * total, eps = SP_EPS * total;
   double before = 0.0;
   int owner = -1;
+#pragma unroll 1
   for (int c = 0; c < a.nc && owner < 0; ++c) {
     const double x = sums[c].a;
     if (before + x > aim) owner = c;
@@ -1208,14 +1215,12 @@ __device__ bool sq_row(const SpSrc<BF16, RES> &src, float *stack, int base, floa
           sure = after - aim > eps && aim - (after - w_hit) > eps;
         }
       }
-      if (lane == 0) {
-        const bool good = hit >= 0 && sure;
-        if (good) {
-          a.token[t] = base + s0 + hit;
-          if (a.prob) a.prob[t] = (float)(w_hit / total);
-        }
-        push_all(&sh->push[4][0], SpPush{0.0, 0.0, 0.0f, good ? 0 : 1}, a.nc);
+      const bool good = hit >= 0 && sure;
+      if (good && lane == 0) {
+        a.token[t] = base + s0 + hit;
+        if (a.prob) a.prob[t] = (float)(w_hit / total);
       }
+      push_all(&sh->push[4][0], SpPush{0.0, 0.0, 0.0f, good ? 0 : 1}, a.nc);
     }
   }
   dense::cluster_sync();
@@ -1272,6 +1277,8 @@ __global__ void __launch_bounds__(SP_THREADS, RES ? 1 : 2) sample_kernel(SpArgs 
   const int rank = (int)dense::cluster_rank(), t = blockIdx.x / a.nc;
   const int base = min(a.V, rank * a.slice), n = min(a.V, base + a.slice) - base;
 
+  pdl_wait();
+  pdl_launch_dependents();
   const float temp = a.temperature ? a.temperature[t] : 1.0f;
   const int top_k = a.top_k ? a.top_k[t] : 0;
   const float top_p = a.top_p ? a.top_p[t] : 1.0f;
@@ -1296,12 +1303,13 @@ __global__ void __launch_bounds__(SP_THREADS, RES ? 1 : 2) sample_kernel(SpArgs 
   if (wid == 0) {
     mx = warp_max(sh->warp_f[0][lane % SP_WARPS]);
     mn = -warp_max(-sh->warp_f[1][lane % SP_WARPS]);
-    if (lane == 0) push_all(&sh->push[6][rank], SpPush{(double)mx, (double)mn, 0.0f, 0}, a.nc);
+    push_all(&sh->push[6][rank], SpPush{(double)mx, (double)mn, 0.0f, 0}, a.nc);
   }
   dense::cluster_sync();
   SpRow r;
   r.max = -CUDART_INF_F;
   mn = CUDART_INF_F;
+#pragma unroll 1
   for (int c = 0; c < a.nc; ++c) {
     r.max = fmaxf(r.max, (float)sh->push[6][c].a);
     mn = fminf(mn, (float)sh->push[6][c].b);
@@ -1336,6 +1344,7 @@ __global__ void __launch_bounds__(SP_THREADS, RES ? 1 : 2) sample_kernel(SpArgs 
     }
     dense::cluster_sync();
     if (rank == 0 && tid == 0) {
+#pragma unroll 1
       for (int c = 0; c < a.nc; ++c) at = min(at, dense::peer(&sh->part[par], c)->n_in);
       a.token[t] = at;
       if (a.prob) a.prob[t] = 1.0f;
@@ -1377,10 +1386,12 @@ __global__ void __launch_bounds__(SP_THREADS, RES ? 1 : 2) sample_kernel(SpArgs 
   }
   dense::cluster_sync();
   double total = 0.0;
+#pragma unroll 1
   for (int c = 0; c < a.nc; ++c) total += dense::peer(&sh->part[par], c)->in;
   const double target = (double)u * total;
   double before = 0.0;
   int owner = -1, last = 0;
+#pragma unroll 1
   for (int c = 0; c < a.nc && owner < 0; ++c) {
     const double s = dense::peer(&sh->part[par], c)->in;
     if (s > 0.0) last = c;
@@ -1470,21 +1481,8 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   const int smem = smem_of(res, seg);
   SpArgs args{logits, temperature, top_p, min_p, u, top_k, token, prob, dev_status, ld, T, V, slice, nc, seg, (seg + SQ_ROUND - 1) / SQ_ROUND};
   const void *fn = kernel(res);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return dense::launched(e);
   void *params[] = {&args};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)T * (unsigned)nc);
-  cfg.blockDim = dim3(SP_THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = nc;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelExC(&cfg, fn, params);
-  note_launch();
-  return dense::launched(e);
+  return dense::launch(fn, T * nc, SP_THREADS, smem, nc, params, (cudaStream_t)stream);
 }

@@ -606,6 +606,48 @@ def test_two_streams_at_once():
     assert q.qmoe_read_status(st) == 0
 
 
+@pytest.mark.parametrize("T,H", [(1, 256), (70, 512), (600, 2048)])
+def test_chained_calls_wait_for_one_another(T, H):
+    """A call may be set up while the one before it runs: every result read or buffer overwritten by the next
+    call, and by other libraries' kernels in between, is as if each had been waited for."""
+    rs = np.random.default_rng(T)
+    x0 = dev(rs.standard_normal((T, H)).astype(np.float32))
+    w = dev((127 * rs.uniform(-1, 1, (H, H))).astype(np.int8))
+    sw = dev((rs.random(H) / 3000).astype(np.float32))
+    wb = dev((rs.standard_normal((H, H)) / H ** 0.5).astype(np.float32), torch.bfloat16)
+    u = dev(uniforms(rs, T))
+
+    def run(wait):
+        x, st = x0.clone(), status_word()
+        norm = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+        codes, scales = torch.empty((T, H), dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+        y, tokens = torch.empty_like(x), []
+        for i in range(12):
+            token = torch.empty(T, dtype=torch.int32, device="cuda")
+            q.qmoe_rmsnorm_residual_q8(x, None, q.F32, None, 1e-6, T, H, 0, None, norm, codes, scales)
+            wait()
+            q.qmoe_linear(codes, q.I8, w, T, H, H, scales, sw, None, q.ACT_SILU, x, x, q.F32, st)   # residual in place
+            wait()
+            codes.zero_()
+            q.qmoe_linear(norm, q.BF16, wb, T, H, H, None, None, None, q.ACT_NONE, None, y, q.F32, st)
+            wait()
+            norm.zero_()
+            q.qmoe_sample(y, q.F32, T, H, None, None, None, None, u, token, None, st)
+            wait()
+            y.mul_(0.5)
+            q.qmoe_rmsnorm_residual_q8(x, y, q.F32, None, 1e-6, T, H, 0, x, None, codes, scales)
+            wait()
+            tokens.append(token)
+        torch.cuda.synchronize()
+        assert q.qmoe_read_status(st) == 0
+        return x, torch.stack(tokens)
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        got = run(lambda: None)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ---------------------------------------------------- behind a layer stack --
 @pytest.mark.parametrize("bits", [8, 16])
 @pytest.mark.parametrize("T", [1, 8])
