@@ -30,6 +30,7 @@ namespace {
 
 constexpr int NQ_VEC = 8;                    // columns per thread and chunk: 16 bytes of bf16, 8 bytes of codes
 constexpr int NQ_MAX_THREADS = 512;
+constexpr int NQ_SMEM = 220 * 1024;          // of an SM, for rows
 constexpr int NQ_MAX_H = 16384, NQ_MAX_T = 1 << 30;
 constexpr float NQ_MAGIC = 12582912.0f;      // 1.5 * 2^23: adding it rounds to an integer, ties to even
 constexpr float NQ_ERR = 3.1e-7f;            // bound of a code's fp32 error relative to it: five roundings of 2^-24
@@ -394,24 +395,28 @@ __global__ void __launch_bounds__(NQ_MAX_THREADS, 2) norm_q8_kernel(const __grid
 }
 
 qmoe_status nq_launch(const NqArgs &a, int dtype, bool norm, cudaStream_t s) {
-  // many rows: 128 threads each, so that a thread's part of the reductions is shared
-  // by more columns; fewer than the SMs hold at once: more, for the shorter chain
-  // (1003 x 5248: 20.5 us with 256, 29.4 with 128, 23.2 with 512; 8192 x 2048: 33.8 with
-  // 128, 38.5 with 256; one row 2.8 with 512, 3.3 with 128)
-  const int nchunk = a.H / NQ_VEC, sms = num_sms();
-  const int most = a.T > 16 * sms ? 128 : a.T > 4 * sms ? 256 : NQ_MAX_THREADS;
+  // Threads per row: many rows 128, so that a thread's part of the reductions is
+  // shared by more columns; fewer rows than the SMs hold at once more, for the shorter
+  // chain (800 x 2048 bf16: 5.8 us with 128, 6.3 with 256; 8192 x 2048: 33.5, 38.5; 400 x
+  // 4096: 6.5 with 256, 7.1 with 512; one row: 2.6 with 512, 3.3 with 128); and enough to
+  // fill an SM with as many CTAs as its shared memory holds (2000 x 4096: 19 us with 256,
+  // 25 with 128; 1100 x 8192: 23 with 512, 32 with 256).
+  const int nchunk = a.H / NQ_VEC, sms = num_sms(), row = a.H * (int)sizeof(float);
+  const int fit = NQ_SMEM / (2 * row);   // CTAs per SM with two rows in turn
+  const int want = a.T > 4 * sms ? 128 : a.T > 2 * sms ? 256 : NQ_MAX_THREADS;
+  const int least = fit >= 8 ? 128 : fit >= 4 ? 256 : NQ_MAX_THREADS, most = want > least ? want : least;
   const int threads = nchunk >= most ? most : (nchunk + 31) / 32 * 32;
   const void *fn = norm ? (dtype == QMOE_BF16 ? (const void *)norm_q8_kernel<true, true> : (const void *)norm_q8_kernel<false, true>)
                         : (dtype == QMOE_BF16 ? (const void *)norm_q8_kernel<true, false> : (const void *)norm_q8_kernel<false, false>);
-  const size_t smem = 2 * (size_t)a.H * sizeof(float);
+  // CTAs that run at once and loop over rows; the widest rows one each (600 x 16384 bf16: 30 us, in turn 58)
+  const long long cap = fit >= 2 ? (long long)(1024 / threads < fit ? 1024 / threads : fit) * sms : a.T;
+  const int grid = a.T < cap ? a.T : (int)cap, smem = (grid < a.T ? 2 : 1) * row;
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return dense::launched(e);
-  const long long cap = 1024LL / threads * sms;
-  const int grid = a.T < cap ? a.T : (int)cap;
   NqArgs args = a;
   void *params[] = {&args};
-  return dense::launch(fn, grid, threads, (int)smem, 1, params, s);
+  return dense::launch(fn, grid, threads, smem, 1, params, s);
 }
 
 bool nq_group_ok(int group, int H) { return group == 0 || ((group == 32 || group == 64 || group == 128) && H % group == 0); }

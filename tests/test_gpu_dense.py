@@ -147,6 +147,19 @@ def test_norm_many_rows(T, H, group, dtype):
     check_norm(xd, None, dtype, None, group)
 
 
+@pytest.mark.parametrize("T,H,group", [(1, 16384, 0), (200, 16384, 128), (330, 8192, 0), (160, 14080, 0), (160, 14096, 0)])
+def test_norm_wide_rows(T, H, group):
+    """Rows in turn in a CTA's shared memory, and rows too wide for that."""
+    rs = np.random.default_rng(H + T)
+    x, y = (rs.standard_normal((T, H)).astype(np.float32) for _ in range(2))
+    x[T // 2] = 0
+    y[T // 2] *= np.float32(1e-40)
+    x[T - 1, H - 1] = 0.5
+    gain = dev((0.2 + rs.random(H)).astype(np.float32))
+    check_norm(dev(x), dev(y), q.F32, gain, group)
+    check_norm(dev(x, torch.bfloat16), None, q.BF16, gain, group)
+
+
 def test_norm_in_place_and_partial_outputs():
     rs = np.random.default_rng(3)
     T, H = 6, 640
