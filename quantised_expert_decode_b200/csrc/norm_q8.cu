@@ -135,8 +135,15 @@ __device__ __forceinline__ void settle(const NqArgs &a, const float *zs, int t, 
   const int h0 = ch * NQ_VEC, lane = threadIdx.x & 31;
   if (a.group != 0) {   // the group's largest |p| in fp32
     uint32_t m = 0;
-#pragma unroll 1
-    for (int h = h0; h < min(h0 + NQ_VEC, a.H); ++h) m = max(m, mag(__fmul_rn(zs[h], nq_gain1(a, h))));
+    if (h0 < a.H) {
+      float z[NQ_VEC], g[NQ_VEC];
+      nq_get(zs, ch, z);
+#pragma unroll
+      for (int i = 0; i < NQ_VEC; ++i) g[i] = 1.0f;
+      if (a.gain) nq_load<false>(a.gain, h0, g);
+#pragma unroll
+      for (int i = 0; i < NQ_VEC; ++i) m = max(m, mag(__fmul_rn(z[i], g[i])));
+    }
     __syncwarp();
     for (int o = a.group / NQ_VEC >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     Af = __uint_as_float(m);
@@ -161,14 +168,13 @@ __device__ __forceinline__ void settle(const NqArgs &a, const float *zs, int t, 
         const double p = (double)z[i] * (double)g[i];
         const float f = floorf(fabsf(v));
         const double left = 254.0 * fabs(p), right = (double)(2.0f * f + 1.0f) * A;
-        int k = (int)f + (left > right ? 1 : 0);
+        // (without a gain both sides are exact, and a tie goes to the even code)
+        int k = (int)f + (left > right || (!a.gain && left == right && ((int)f & 1)) ? 1 : 0);
         k = v < 0.0f ? -k : k;
-        bool tie = false;
-        if (fabs(left - right) <= (exact ? 1e-14 : 1.3e-7) * right) {
-          tie = exact;
-          open |= !exact;
+        if (a.gain && fabs(left - right) <= (exact ? 1e-14 : 1.3e-7) * right) {
+          if (exact) ties |= 1u << i;
+          else open = true;
         }
-        if (tie) ties |= 1u << i;
         a.codes[(size_t)t * a.H + h0 + i] = (int8_t)k;
       }
 #pragma unroll 1

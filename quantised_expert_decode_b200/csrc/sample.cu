@@ -59,6 +59,9 @@ constexpr double SP_EPS = 1e-11;              // bound of the quick sums' error,
 constexpr int SP_LIST = 512;                  // elements ranked one by one (one per thread)
 constexpr int SP_MAX_CLUSTER = 8;             // CTAs per row
 constexpr long long SP_L2_BYTES = 126ll << 20;
+// More CTAs on fewer logits cost more barriers than they save (8 rows of 4000: 14.0 us
+// by one CTA each, 16.4 by two; of 8000: 15.2 by one, 16.4 by two, 16.9 by four).
+constexpr int SP_MIN_SLICE = 4096;
 constexpr int SP_MAX_SLICE = 32768;           // 128 KB of fp32 logits per CTA
 constexpr int SP_MAX_V = 393216, SP_MAX_T = 1 << 27;
 constexpr double SP_W_MIN = 5.421010862427522e-20;   // 2^-64
@@ -1469,11 +1472,11 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   // 139 us, one each 148; of 60000: one each 72 us, two 82).
   const int sms = num_sms();
   int nc = SP_MAX_CLUSTER;
-  while (nc > 1 && (T * (long long)nc > sms || T > dense::max_clusters(nc, kernel(true), SP_THREADS, smem_of(true, SP_MAX_SLICE / SP_WARPS)))) nc /= 2;
+  while (nc > 1 && (V < nc * SP_MIN_SLICE || T * (long long)nc > sms || T > dense::max_clusters(nc, kernel(true), SP_THREADS, smem_of(true, SP_MAX_SLICE / SP_WARPS)))) nc /= 2;
   const bool res = T <= sms && (V + nc - 1) / nc <= SP_MAX_SLICE;
   if (!res) {
     nc = 1;
-    while (nc < SP_MAX_CLUSTER && T * (long long)nc <= sms) nc *= 2;
+    while (nc < SP_MAX_CLUSTER && T * (long long)nc <= sms && V >= 2 * nc * SP_MIN_SLICE) nc *= 2;
     if (nc == 1 && 2LL * sms * V * (dtype == QMOE_BF16 ? 2 : 4) > SP_L2_BYTES) nc = 2;
   }
   const int slice = ((V + nc - 1) / nc + 7) / 8 * 8;
