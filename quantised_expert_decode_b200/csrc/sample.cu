@@ -1472,7 +1472,9 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   // 139 us, one each 148; of 60000: one each 72 us, two 82).
   const int sms = num_sms();
   int nc = SP_MAX_CLUSTER;
-  while (nc > 1 && (V < nc * SP_MIN_SLICE || T * (long long)nc > sms || T > dense::max_clusters(nc, kernel(true), SP_THREADS, smem_of(true, SP_MAX_SLICE / SP_WARPS)))) nc /= 2;
+  while (nc > 1 && (V < nc * SP_MIN_SLICE || T * (long long)nc > sms ||
+                    T > dense::max_clusters(nc, kernel(true), SP_THREADS, smem_of(true, SP_MAX_SLICE / SP_WARPS))))
+    nc /= 2;
   const bool res = T <= sms && (V + nc - 1) / nc <= SP_MAX_SLICE;
   if (!res) {
     nc = 1;
@@ -1482,7 +1484,8 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   const int slice = ((V + nc - 1) / nc + 7) / 8 * 8;
   const int seg = (slice + SP_WARPS * 128 - 1) / (SP_WARPS * 128) * 128;
   const int smem = smem_of(res, seg);
-  SpArgs args{logits, temperature, top_p, min_p, u, top_k, token, prob, dev_status, ld, T, V, slice, nc, seg, (seg + SQ_ROUND - 1) / SQ_ROUND};
+  SpArgs args{logits, temperature, top_p, min_p, u,     top_k, token, prob, dev_status,
+              ld,     T,           V,     slice, nc,    seg,   (seg + SQ_ROUND - 1) / SQ_ROUND};
   const void *fn = kernel(res);
   const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return dense::launched(e);
