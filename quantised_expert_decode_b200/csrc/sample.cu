@@ -1280,6 +1280,7 @@ __global__ void __launch_bounds__(SP_THREADS, RES ? 1 : 2) sample_kernel(SpArgs 
   const int rank = (int)dense::cluster_rank(), t = blockIdx.x / a.nc;
   const int base = min(a.V, rank * a.slice), n = min(a.V, base + a.slice) - base;
 
+  dense::cluster_arrive();   // (waited for before the first store into another CTA)
   pdl_wait();
   pdl_launch_dependents();
   const float temp = a.temperature ? a.temperature[t] : 1.0f;
@@ -1303,6 +1304,7 @@ __global__ void __launch_bounds__(SP_THREADS, RES ? 1 : 2) sample_kernel(SpArgs 
     sh->warp_f[1][wid] = mn;
   }
   __syncthreads();
+  dense::cluster_wait();   // every CTA of the cluster is running: its shared memory may be written
   if (wid == 0) {
     mx = warp_max(sh->warp_f[0][lane % SP_WARPS]);
     mn = -warp_max(-sh->warp_f[1][lane % SP_WARPS]);

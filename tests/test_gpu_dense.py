@@ -528,6 +528,39 @@ def test_sample_more_rows_than_sms(dtype):
     check_sample(l, dtype, u=u, min_p=rs.random(T) ** 3, top_p=0.5 + 0.5 * rs.random(T), top_k=rs.integers(0, 3000, T))
 
 
+@pytest.mark.parametrize("T,V", [(1, 8192), (61, 9001), (61, 32003), (3, 16384), (36, 20011), (2, 32768), (15, 33001)])
+@pytest.mark.parametrize("dtype", [q.F32, q.BF16])
+def test_sample_by_clusters_of_every_size(T, V, dtype):
+    """Rows by two, four and eight CTAs with short slices; greedy and masked rows, and each filter."""
+    rs = np.random.default_rng(T * 7 + V + dtype)
+    l = (2.5 * rs.standard_normal((T, V))).astype(np.float32)
+    l[rs.random((T, V)) < 0.3] = -np.inf
+    l[:, V // 2] = 1.0                                       # at least one candidate
+    if T > 10:
+        l[4], l[9] = -np.inf, 3.0                            # nothing, and all the same
+        l[7, :V - 5] = -np.inf                               # all of it in the last slice
+    temp = (0.5 + rs.random(T)).astype(np.float32)
+    temp[::4] = 0
+    u = uniforms(rs, T)
+    check_sample(l, dtype, u=u, temperature=temp, min_p=0.05 * rs.random(T))
+    check_sample(l, dtype, u=u, temperature=temp, top_p=0.5 + 0.5 * rs.random(T))
+    check_sample(l, dtype, u=u, top_k=rs.integers(1, 60, T), top_p=np.full(T, 0.9), min_p=np.full(T, 0.01))
+
+
+@pytest.mark.parametrize("T,V,dtype", [(160, 131072, q.F32), (151, 111601, q.F32), (150, 262145, q.BF16)])
+def test_sample_streamed_clusters_in_turns(T, V, dtype):
+    """More rows than SMs, too large for L2 together: two CTAs per row, more clusters than run at once."""
+    rs = np.random.default_rng(V + T)
+    l = (2.5 * rs.standard_normal((T, V), dtype=np.float32)).astype(np.float32)
+    l[3] = -np.inf
+    l[5, rs.random(V) < 0.99] = -np.inf
+    l[6] *= np.float32(0.01)
+    temp = (0.5 + rs.random(T)).astype(np.float32)
+    temp[::16] = 0
+    check_sample(l, dtype, u=uniforms(rs, T), temperature=temp, top_p=0.5 + 0.5 * rs.random(T))
+    check_sample(l, dtype, u=uniforms(rs, T), top_k=rs.integers(0, 1500, T), min_p=0.02 * rs.random(T))
+
+
 def test_sample_is_repeatable():
     rs = np.random.default_rng(9)
     l = dev((2 * rs.standard_normal((7, 60000))).astype(np.float32))
