@@ -210,10 +210,41 @@ _TORCH_TYPES: dict = {}
 _DTYPES = {F32: "float32", BF16: "bfloat16", I8: "int8"}
 
 
+def _misfit(t, rows, cols, ld) -> str | None:
+    """Why a tensor's own shape and strides are not ``rows`` rows of ``cols`` dense elements, ``ld`` elements from
+    one to the next (0: a vector of ``cols``). What lies in its storage beside it does not count."""
+    def run(dims):   # (size, stride) of dimensions that are one run, outermost first; sizes of 1 have no stride
+        dims = [d for d in dims if d[0] > 1]
+        if any(a[1] != b[0] * b[1] for a, b in zip(dims, dims[1:])):
+            return None
+        size = 1
+        for d in dims:
+            size *= d[0]
+        return size, dims[-1][1] if dims else None
+    shape, strides = t.shape, t.stride()
+    if ld and len(shape) == 2 and strides == (ld, 1) and shape[0] >= rows and shape[1] >= cols:   # (most that get here)
+        return None
+    dims = list(zip(shape, strides))
+    lead, width = dims[:-1], dims[-1] if dims else (1, 1)
+    if ld and any(n > 1 for n, _ in lead):
+        at = run(lead)
+        if width[1] != 1 and width[0] > 1:
+            return "whose rows are not contiguous"
+        if at is None or at[1] != ld:
+            return "whose row stride is not the one given"
+        return None if at[0] >= rows and width[0] >= cols else "smaller than the call's sizes"
+    # one run: a vector, a single row, or a flat buffer of rows
+    at = run(dims)
+    if at is None or at[1] not in (None, 1):
+        return "whose rows are not contiguous"
+    return None if t.numel() >= (rows - 1) * (ld or cols) + cols else "smaller than the call's sizes"
+
+
 def _fits(fn: str, *wants) -> list:
-    """(tensor or None, type, rows, columns, row stride) each: on the current device, of the type, rows dense,
-    and large enough for what the call reads or writes. A plain address (int) is the caller's word. Returns
-    their addresses (one pass over the tensors: a short kernel takes less time than asking them twice)."""
+    """(tensor or None, type, rows, columns, row stride) each: on the current device, of the type, rows dense and
+    at one stride, and large enough by its own shape for what the call reads or writes. A plain address (int) is
+    the caller's word. Returns their addresses (one pass over the tensors: a short kernel takes less time than
+    asking them twice)."""
     import torch
     if not _TORCH_TYPES:
         _TORCH_TYPES.update((name, getattr(torch, name)) for name in ("float32", "bfloat16", "int8", "int32"))
@@ -234,12 +265,9 @@ def _fits(fn: str, *wants) -> list:
             raise QmoeError(fn + f" (a {t.dtype} tensor in the place of a {dtype} one)", 1)
         if t.get_device() != dev:
             raise QmoeError(fn + " (a tensor on another device than the current one)", 1)
-        if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
-            raise QmoeError(fn + " (a tensor whose rows are not contiguous)", 1)
-        if t.dim() > 1 and ld and t.shape[-2] > 1 and t.stride(-2) != ld:
-            raise QmoeError(fn + " (a tensor whose row stride is not the one given)", 1)
-        if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < (rows - 1) * (ld or cols) + cols:
-            raise QmoeError(fn + " (a tensor smaller than the call's sizes)", 1)
+        wrong = _misfit(t, rows, cols, ld)
+        if wrong:
+            raise QmoeError(f"{fn} (a tensor {wrong})", 1)
         out.append(t.data_ptr())
     return out
 

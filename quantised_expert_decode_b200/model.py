@@ -147,7 +147,9 @@ class TokenHead:
 
     def step(self, x, u, temperature=None, top_k=None, top_p=None, min_p=None, y=None, stream=None) -> torch.Tensor:
         """``x`` (and ``y``, added to it) fp32 or bf16 [T, H], for instance ``DecodeStack.x_out``; ``u`` fp32 [T] in
-        [0, 1), one per row; the rest as in qmoe_sample. Returns the device tensor ``token`` int32 [T]."""
+        [0, 1), one per row; the rest as in qmoe_sample. Rows lie one behind the other: the last positions of
+        [T, S, H] hidden states go in as ``hidden[:, -1].contiguous()``, and as a view they are refused. Returns
+        the device tensor ``token`` int32 [T]."""
         if x.dtype not in (torch.bfloat16, torch.float32):
             raise L.QmoeError("TokenHead.step (x must be bf16 or fp32)", 1)
         if x.numel() != self.T * self.H:

@@ -127,3 +127,60 @@ def test_binding_refuses_tensors_that_do_not_fit(monkeypatch):
                 (x, "bfloat16", 4, 64, 64), (x.double(), f, 4, 64, 64), (_OnAnotherDevice(), f, 1, 1, 0)):
         with pytest.raises(q.QmoeError):
             L._fits("f", bad)
+
+
+def _fits_on_cpu(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # CPU tensors report device -1
+    return torch, "float32"
+
+
+def test_binding_refuses_rows_that_are_not_at_one_stride(monkeypatch):
+    """Views whose rows do not follow one another at the stride that the call reads with."""
+    torch, f = _fits_on_cpu(monkeypatch)
+    h = torch.zeros(4, 8, 64)
+    bad = {"last position of each sequence": (h[:, -1:, :], f, 4, 64, 64),
+           "the same, squeezed": (h[:, -1], f, 4, 64, 64),
+           "two positions of each sequence": (h[:, :2], f, 8, 64, 64),
+           "heads apart": (torch.zeros(4, 2, 96)[:, :, :64], f, 8, 64, 64),
+           "transposed heads": (torch.zeros(2, 4, 64).transpose(0, 1), f, 8, 64, 64),
+           "broadcast rows": (torch.zeros(1, 64).expand(4, 64), f, 4, 64, 64),
+           "narrower rows than the call's": (torch.zeros(4, 32), f, 2, 64, 64),
+           "a column of rows": (torch.zeros(6, 4)[:, :1], f, 1, 6, 0),
+           "a column": (torch.zeros(6, 4)[:, 1], f, 1, 6, 0),
+           "packed scales in wider rows": (torch.zeros(6, 10)[:, :4], f, 1, 24, 0),
+           "one value broadcast": (torch.zeros(1).expand(6), f, 1, 6, 0)}
+    for name, want in bad.items():
+        with pytest.raises(q.QmoeError):
+            L._fits("f", want)
+            pytest.fail(name)
+    for good in ((h, f, 32, 64, 64), (h[1], f, 8, 64, 64), (h[1:3], f, 16, 64, 64), (h[:1, -1:, :], f, 1, 64, 64),
+                 (h[:, -1], f, 4, 64, 512), (h[:, -1:, :], f, 4, 64, 512), (h.view(-1), f, 32, 64, 64),
+                 (h.view(-1), f, 4, 64, 500), (h.view(32, 64)[:, :50], f, 32, 50, 64), (h.view(32, 64), f, 32, 50, 64),
+                 (torch.zeros(6, 1), f, 1, 6, 0), (torch.zeros(1, 6, 1), f, 1, 6, 0), (torch.zeros(6, 4), f, 1, 24, 0),
+                 (torch.zeros(8, 1)[2:], f, 1, 6, 0), (torch.zeros(3, 1, 5)[1], f, 1, 5, 0),
+                 (torch.zeros(6, 4)[2, :1], f, 1, 1, 0), (torch.nn.Parameter(torch.zeros(4, 64)), f, 4, 64, 64)):
+        assert L._fits("f", good) == [good[0].data_ptr()]
+
+
+def test_binding_refuses_views_shorter_than_the_call(monkeypatch):
+    """What lies behind a view in its storage belongs to someone else."""
+    torch, f = _fits_on_cpu(monkeypatch)
+    x, u = torch.zeros(16, 64), torch.zeros(12)
+    for bad in ((x[:2], f, 4, 64, 64), (x[:2, :50], f, 4, 50, 64), (x[:4, :40], f, 4, 50, 64), (u[:2], f, 1, 6, 0),
+                (u[:0], f, 1, 1, 0), (x.view(-1)[:200], f, 4, 64, 64), (x[:4, :50], f, 5, 50, 64), (u[:0], f, 1, 6, 0)):
+        with pytest.raises(q.QmoeError):
+            L._fits("f", bad)
+    L._fits("f", (x[:4], f, 4, 64, 64), (u[:6], f, 1, 6, 0), (x[:4, :50], f, 4, 50, 64), (x.view(-1)[:192 + 50], f, 4, 50, 64))
+
+
+def test_token_head_refuses_hidden_states_of_scattered_rows(monkeypatch):
+    torch, f = _fits_on_cpu(monkeypatch)
+    from quantised_expert_decode_b200.model import TokenHead
+    head = TokenHead.__new__(TokenHead)
+    head.T, head.H, head.gain, head.eps, head.bits, head.norm = 4, 64, None, 1e-6, 8, None
+    head.codes, head.scale = torch.zeros((4, 64), dtype=torch.int8), torch.zeros(4)
+    h = torch.zeros(4, 8, 64)
+    for x in (h[:, -1:, :], h[:, -1], h[:, ::8]):
+        with pytest.raises(q.QmoeError, match="row"):
+            head.step(x, torch.zeros(4))
