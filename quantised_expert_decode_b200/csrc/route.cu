@@ -30,7 +30,7 @@ constexpr int RT_THREADS = 32 * RT_WARPS;
 constexpr int RT_MAXT = 8;
 constexpr int RT_GROUP = 32;               // experts per CTA, one per lane
 constexpr int RT_CHUNK = 16;               // slices staged in shared memory at a time
-constexpr int RT_PRE = 2;                  // slices per warp whose weights are fetched before the wait
+constexpr int RT_PRE = 2;                  // slices per warp whose weights are fetched ahead of the activations
 static_assert(RT_CHUNK * 16 == 32 * RT_WARPS, "a whole chunk is one element per thread and token");
 
 struct RouteArgs {
@@ -42,6 +42,7 @@ struct RouteArgs {
   float eps;
   int T, H, E, k;
   int ns;              // hidden-axis ranges per expert group
+  bool wr_early;       // nothing on the stream writes Wr: its first slices may be read before the wait
   int32_t *idx;
   float *gate;
   unsigned long long *lacc;   // workspace [T][E] exact partial-logit sums (2^-32 units, two's complement)
@@ -160,19 +161,24 @@ __global__ void __launch_bounds__(RT_THREADS, 1) route_decode_kernel(RouteArgs a
   const int c0 = (int)((long long)sp * nsl / a.ns), c1 = (int)((long long)(sp + 1) * nsl / a.ns);
   const float4 *wrow = reinterpret_cast<const float4 *>(a.Wr + (size_t)(live ? e : 0) * H);
 
-  // The first slices' weights do not depend on the previous kernel: fetch
-  // them before waiting for it.
+  // The first slices' weights. Inside a stack nothing writes Wr, and they are
+  // fetched before the wait for the previous kernel; a caller's previous kernel
+  // may be the one that writes Wr, and may have let this one start before it does.
   float4 wpre[RT_PRE][4];
+  auto fetch_first = [&] {
 #pragma unroll
-  for (int m = 0; m < RT_PRE; ++m) {
-    const int c = c0 + warp + RT_WARPS * m;
+    for (int m = 0; m < RT_PRE; ++m) {
+      const int c = c0 + warp + RT_WARPS * m;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      wpre[m][q] = (live && c < c1 && c < c0 + RT_CHUNK) ? __ldg(wrow + c * 4 + q) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+      for (int q = 0; q < 4; ++q)
+        wpre[m][q] = (live && c < c1 && c < c0 + RT_CHUNK) ? __ldg(wrow + c * 4 + q) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  if (a.wr_early) fetch_first();
   if (tid == 0) range_bad = 0;
   pdl_wait();
   pdl_launch_dependents();
+  if (!a.wr_early) fetch_first();
 
   long long acc[TT];
 #pragma unroll
@@ -393,18 +399,22 @@ extern "C" size_t qmoe_route_workspace_bytes(int T, int E) {
   return route_prefill_ws_bytes(T, E);
 }
 
-extern "C" qmoe_status qmoe_route(const float *Wr, const float *bias, const void *x, int x_dtype, int T, int H, int E,
-                                  int k, int32_t *idx, float *gate, void *workspace, size_t workspace_bytes,
-                                  int32_t *dev_status, qmoe_stream_t stream) {
+namespace qmoe {
+
+// The calls below, and the same from inside a captured stack (wr_early: Wr is
+// written by nothing that the stream's previous kernel may still be doing).
+qmoe_status route_call(const float *Wr, const float *bias, const void *x, int x_dtype, int T, int H, int E, int k,
+                       int32_t *idx, float *gate, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                       cudaStream_t stream, bool wr_early) {
   qmoe_status st = check_route_common(Wr, T, H, E, k, idx, gate, workspace, dev_status);
   if (st != QMOE_OK) return st;
   if (!x || !aligned16(x)) return QMOE_ERR_INVALID_ARG;
   if (x_dtype != QMOE_F32 && x_dtype != QMOE_BF16) return QMOE_ERR_INVALID_ARG;
   if (workspace_bytes < qmoe_route_workspace_bytes(T, E)) return QMOE_ERR_WORKSPACE;
   if (T > RT_MAXT || x_dtype == QMOE_BF16)
-    return route_prefill(Wr, bias, x, x_dtype, T, H, E, k, idx, gate, workspace, workspace_bytes, dev_status,
-                         (cudaStream_t)stream);
+    return route_prefill(Wr, bias, x, x_dtype, T, H, E, k, idx, gate, workspace, workspace_bytes, dev_status, stream);
   RouteArgs a{};
+  a.wr_early = wr_early;
   a.Wr = Wr;
   a.bias = bias;
   a.x = static_cast<const float *>(x);
@@ -414,13 +424,13 @@ extern "C" qmoe_status qmoe_route(const float *Wr, const float *bias, const void
   a.lacc = static_cast<unsigned long long *>(workspace);
   a.ticket = reinterpret_cast<unsigned *>(static_cast<char *>(workspace) + decode_lacc_bytes(T, E));
   a.status = dev_status;
-  return launch_route_decode(a, false, (cudaStream_t)stream);
+  return launch_route_decode(a, false, stream);
 }
 
-extern "C" qmoe_status qmoe_residual_route(const float *x_in, const float *y, float eps, float *x_out, const float *Wr,
-                                           const float *bias, int T, int H, int E, int k, int32_t *idx, float *gate,
-                                           void *workspace, size_t workspace_bytes, int32_t *dev_status,
-                                           qmoe_stream_t stream) {
+qmoe_status residual_route_call(const float *x_in, const float *y, float eps, float *x_out, const float *Wr,
+                                const float *bias, int T, int H, int E, int k, int32_t *idx, float *gate,
+                                void *workspace, size_t workspace_bytes, int32_t *dev_status, cudaStream_t stream,
+                                bool wr_early) {
   qmoe_status st = check_route_common(Wr, T, H, E, k, idx, gate, workspace, dev_status);
   if (st != QMOE_OK) return st;
   if (!x_in || !y || !x_out || !aligned16(x_in) || !aligned16(y) || !aligned16(x_out)) return QMOE_ERR_INVALID_ARG;
@@ -429,6 +439,7 @@ extern "C" qmoe_status qmoe_residual_route(const float *x_in, const float *y, fl
   if (T > RT_MAXT) return QMOE_ERR_UNSUPPORTED;
   if (workspace_bytes < qmoe_route_workspace_bytes(T, E)) return QMOE_ERR_WORKSPACE;
   RouteArgs a{};
+  a.wr_early = wr_early;
   a.Wr = Wr;
   a.bias = bias;
   a.x = x_in;
@@ -441,7 +452,24 @@ extern "C" qmoe_status qmoe_residual_route(const float *x_in, const float *y, fl
   a.lacc = static_cast<unsigned long long *>(workspace);
   a.ticket = reinterpret_cast<unsigned *>(static_cast<char *>(workspace) + decode_lacc_bytes(T, E));
   a.status = dev_status;
-  return launch_route_decode(a, true, (cudaStream_t)stream);
+  return launch_route_decode(a, true, stream);
+}
+
+}  // namespace qmoe
+
+extern "C" qmoe_status qmoe_route(const float *Wr, const float *bias, const void *x, int x_dtype, int T, int H, int E,
+                                  int k, int32_t *idx, float *gate, void *workspace, size_t workspace_bytes,
+                                  int32_t *dev_status, qmoe_stream_t stream) {
+  return route_call(Wr, bias, x, x_dtype, T, H, E, k, idx, gate, workspace, workspace_bytes, dev_status,
+                    (cudaStream_t)stream, false);
+}
+
+extern "C" qmoe_status qmoe_residual_route(const float *x_in, const float *y, float eps, float *x_out, const float *Wr,
+                                           const float *bias, int T, int H, int E, int k, int32_t *idx, float *gate,
+                                           void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                           qmoe_stream_t stream) {
+  return residual_route_call(x_in, y, eps, x_out, Wr, bias, T, H, E, k, idx, gate, workspace, workspace_bytes,
+                             dev_status, (cudaStream_t)stream, false);
 }
 
 // ----------------------------------------------------------- fixed scratch --

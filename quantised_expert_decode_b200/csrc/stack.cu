@@ -11,6 +11,12 @@ namespace qmoe {
 qmoe_status ffn_decode_launch(const qmoe_experts *ex, const float *x, int T, const int32_t *idx, const float *gate,
                               int k, float *y, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t s,
                               bool cooperative);
+qmoe_status route_call(const float *Wr, const float *bias, const void *x, int x_dtype, int T, int H, int E, int k,
+                       int32_t *idx, float *gate, void *ws, size_t ws_bytes, int32_t *status, cudaStream_t s,
+                       bool wr_early);
+qmoe_status residual_route_call(const float *x_in, const float *y, float eps, float *x_out, const float *Wr,
+                                const float *bias, int T, int H, int E, int k, int32_t *idx, float *gate, void *ws,
+                                size_t ws_bytes, int32_t *status, cudaStream_t s, bool wr_early);
 }
 
 struct qmoe_stack {
@@ -102,13 +108,13 @@ qmoe_status record(qmoe_stack *s, cudaStream_t cs, bool coop) {
     const float *bias = s->bias[l];
     const float *x_cur;
     if (l == 0) {
-      st = qmoe_route(s->Wr[l], bias, s->x_in, QMOE_F32, s->T, s->H, s->E, s->k, idx, gate, s->route_ws,
-                      s->route_ws_bytes, s->status, (qmoe_stream_t)cs);
+      st = qmoe::route_call(s->Wr[l], bias, s->x_in, QMOE_F32, s->T, s->H, s->E, s->k, idx, gate, s->route_ws,
+                            s->route_ws_bytes, s->status, cs, true);
       x_cur = s->x_in;
     } else {
       float *xo = (l & 1) ? s->xa : s->xb;
-      st = qmoe_residual_route(x_prev, s->y, s->eps, xo, s->Wr[l], bias, s->T, s->H, s->E, s->k, idx, gate,
-                               s->route_ws, s->route_ws_bytes, s->status, (qmoe_stream_t)cs);
+      st = qmoe::residual_route_call(x_prev, s->y, s->eps, xo, s->Wr[l], bias, s->T, s->H, s->E, s->k, idx, gate,
+                                     s->route_ws, s->route_ws_bytes, s->status, cs, true);
       x_cur = xo;
     }
     if (st != QMOE_OK) return st;

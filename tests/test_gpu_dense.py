@@ -694,6 +694,51 @@ def test_chained_calls_wait_for_one_another(T, H):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("how", ["route", "residual_route", "route_fixed"])
+@pytest.mark.parametrize("captured", [False, True])
+def test_router_weights_written_by_the_call_before(how, captured):
+    """The router reads the weights that a product on the same stream has just written, and its inputs too."""
+    rs = np.random.default_rng(21)
+    E, H, K, T, k = 256, 512, 65536, 4, 8
+    w = dev(rs.standard_normal((H, K), dtype=np.float32), torch.bfloat16)
+    a = dev(rs.standard_normal((E, K), dtype=np.float32) / 256, torch.bfloat16)
+    sides = [a, -a, a.flip(0).contiguous()]
+    x, y = (dev(rs.standard_normal((T, H)).astype(np.float32)) for _ in range(2))
+    ws, st = torch.zeros(q.qmoe_route_workspace_bytes(T, E), dtype=torch.uint8, device="cuda"), status_word()
+    Wr, x_out = torch.empty((E, H), device="cuda"), torch.empty_like(x)
+
+    def run(wait):
+        got = []
+        for i in range(9):
+            idx, gate = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+            q.qmoe_linear(sides[i % 3], q.BF16, w, E, H, K, None, None, None, q.ACT_NONE, None, Wr, q.F32, st)
+            wait()
+            if how == "route":
+                q.qmoe_route(Wr, None, x, q.F32, T, H, E, k, idx, gate, ws, st)
+            elif how == "route_fixed":
+                q.qmoe_route_fixed(Wr, None, x, T, H, E, k, idx, gate, st)
+            else:
+                q.qmoe_residual_route(x, y, 1e-6, x_out, Wr, None, T, H, E, k, idx, gate, ws, st)
+            wait()
+            got.append((idx, gate))
+        return got
+
+    want = run(torch.cuda.synchronize)
+    assert not torch.equal(want[0][0], want[1][0])
+    for _ in range(3):
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                got = run(lambda: None)
+            graph.replay()
+        else:
+            got = run(lambda: None)
+        torch.cuda.synchronize()
+        for (i, g), (wi, wg) in zip(got, want):
+            assert torch.equal(i, wi) and torch.equal(g, wg)
+    assert q.qmoe_read_status(st) == 0
+
+
 # ---------------------------------------------------- behind a layer stack --
 @pytest.mark.parametrize("bits", [8, 16])
 @pytest.mark.parametrize("T", [1, 8])
