@@ -31,6 +31,7 @@ namespace {
 constexpr int NQ_VEC = 8;                    // columns per thread and chunk: 16 bytes of bf16, 8 bytes of codes
 constexpr int NQ_MAX_THREADS = 512;
 constexpr int NQ_SMEM = 220 * 1024;          // of an SM, for rows
+constexpr int NQ_MAX_CTA_SMEM = NQ_SMEM / 2; // of a CTA: two rows in turn only where two CTAs fit
 constexpr int NQ_MAX_H = 16384, NQ_MAX_T = 1 << 30;
 constexpr float NQ_MAGIC = 12582912.0f;      // 1.5 * 2^23: adding it rounds to an integer, ties to even
 constexpr float NQ_ERR = 3.1e-7f;            // bound of a code's fp32 error relative to it: five roundings of 2^-24
@@ -418,7 +419,9 @@ qmoe_status nq_launch(const NqArgs &a, int dtype, bool norm, cudaStream_t s) {
   const long long cap = fit >= 2 ? (long long)(1024 / threads < fit ? 1024 / threads : fit) * sms : a.T;
   const int grid = a.T < cap ? a.T : (int)cap, smem = (grid < a.T ? 2 : 1) * row;
   cudaError_t e = cudaSuccess;
-  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the largest a call can need, not this call's: the limit is the kernel's, for all host threads)
+  static_assert(NQ_MAX_H * sizeof(float) <= NQ_MAX_CTA_SMEM, "one of the widest rows");
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, NQ_MAX_CTA_SMEM);
   if (e != cudaSuccess) return dense::launched(e);
   NqArgs args = a;
   void *params[] = {&args};

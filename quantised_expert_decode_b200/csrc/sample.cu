@@ -1489,7 +1489,9 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   SpArgs args{logits, temperature, top_p, min_p, u,     top_k, token, prob, dev_status,
               ld,     T,           V,     slice, nc,    seg,   (seg + SQ_ROUND - 1) / SQ_ROUND};
   const void *fn = kernel(res);
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the largest a call can need, not this call's: the limit is the kernel's, for all host threads)
+  const cudaError_t e =
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(res, SP_MAX_SLICE / SP_WARPS));
   if (e != cudaSuccess) return dense::launched(e);
   void *params[] = {&args};
   return dense::launch(fn, T * nc, SP_THREADS, smem, nc, params, (cudaStream_t)stream);

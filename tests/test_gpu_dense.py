@@ -13,6 +13,9 @@ Tolerances (u = 2^-24, half an fp32 step relative to the value):
   truncate by a step (2 u) of at most sum |a w|. Activations have a slope of at
   most 1.13 and are formed to 2e-6 of |v|.
 """
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -649,6 +652,59 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for d, t, (o, k) in zip(ds, toks, want):
         assert torch.equal(d["out"], o) and torch.equal(t, k)
+    assert q.qmoe_read_status(st) == 0
+
+
+@pytest.mark.parametrize("op", ["norm", "quantise", "sample"])
+def test_two_host_threads_with_calls_of_different_sizes(op):
+    """Neither thread's calls are refused for the size of the other's, and each gets its own results. (The C calls
+    themselves: between two calls of the binding the threads hardly ever meet.)"""
+    rs, lib, p = np.random.default_rng(14), q.lib(), ctypes.c_void_p
+    u, st = dev(np.float32([0.4])), status_word()
+    keep, calls = [], []
+    for n in range(2):
+        stream = torch.cuda.Stream()
+        size = ((8000, 131072) if op == "sample" else (11008, 16384))[n]
+        x = dev(rs.standard_normal((1, size)).astype(np.float32))
+        out = torch.zeros((1, size), dtype=torch.int8, device="cuda")
+        value = torch.zeros(1, dtype=torch.int32 if op == "sample" else torch.float32, device="cuda")
+        px, po, pv, ps = (p(t) for t in (x.data_ptr(), out.data_ptr(), value.data_ptr(), stream.cuda_stream))
+        if op == "sample":
+            args = (lib.qmoe_sample, px, q.F32, 1, size, 0, None, None, None, None, p(u.data_ptr()), pv, None, p(st.data_ptr()), ps)
+        elif op == "quantise":
+            args = (lib.qmoe_quantise_rows, px, q.F32, 1, size, 0, po, pv, ps)
+        else:
+            args = (lib.qmoe_rmsnorm_residual_q8, px, None, q.F32, None, 1e-6, 1, size, 0, None, None, po, pv, ps)
+        keep.append((x, stream, out, value))
+        calls.append(args)
+    torch.cuda.synchronize()
+    want = []
+    for args, (_, _, out, value) in zip(calls, keep):
+        assert args[0](*args[1:]) == 0
+        torch.cuda.synchronize()
+        want.append((out.clone(), value.clone()))
+        out.zero_(), value.zero_()
+    torch.cuda.synchronize()
+    go, refused = threading.Barrier(2), [0, 0]
+
+    def work(n):
+        torch.cuda.set_device(0)
+        call, args = calls[n][0], calls[n][1:]
+        go.wait(20)
+        for i in range(8000):
+            refused[n] += call(*args) != 0
+            if i % 500 == 0:
+                keep[n][1].synchronize()
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert refused == [0, 0]
+    for (_, _, out, value), (o, v) in zip(keep, want):
+        assert torch.equal(out, o) and torch.equal(value, v)
     assert q.qmoe_read_status(st) == 0
 
 
