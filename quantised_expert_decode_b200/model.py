@@ -111,8 +111,8 @@ class TokenHead:
 
     ``weight`` bf16 or fp32 [V, H]. With ``bits`` 8 its rows are kept as int8 codes and fp32 scales
     (qmoe_quantise_rows) and the normed rows are 8-bit too; with ``bits`` 16 both are bf16. ``gain`` fp32 [H]
-    or None; ``bias`` fp32 [V] or None. All buffers are made here; ``step`` only launches, and can be captured.
-    Two steps that overlap on different streams need a head each.
+    or None; ``bias`` fp32 [V] or None. All buffers are made here, on ``stream`` where one is given; ``step`` only
+    launches, and can be captured. Two steps that overlap on different streams need a head each.
     """
 
     def __init__(self, weight, T: int, gain=None, bias=None, eps: float = 1e-6, bits: int = 8, stream=None):
@@ -124,12 +124,25 @@ class TokenHead:
             raise L.QmoeError("TokenHead (no tokens)", 1)
         self.V, self.H = weight.shape
         self.T, self.eps, self.bits, self.gain, self.bias = T, eps, bits, gain, bias
-        dev = weight.device
-        if bits == 8:
+        if stream is None:
+            self._lay_out(weight)
+            return
+        # every buffer made and filled on the given stream, behind what has been queued on the current one (the
+        # weights, for instance), which in turn goes on behind it: the weights may be dropped after this
+        own = torch.cuda.ExternalStream(stream, device=weight.device) if isinstance(stream, int) else stream
+        here = torch.cuda.current_stream(weight.device)
+        own.wait_stream(here)
+        with torch.cuda.stream(own):
+            self._lay_out(weight)
+        here.wait_stream(own)
+
+    def _lay_out(self, weight) -> None:
+        T, dev = self.T, weight.device
+        if self.bits == 8:
             self.weight = torch.empty((self.V, self.H), dtype=torch.int8, device=dev)
             self.weight_scale = torch.empty(self.V, dtype=torch.float32, device=dev)
             L.qmoe_quantise_rows(weight, L.BF16 if weight.dtype == torch.bfloat16 else L.F32, self.V, self.H, 0,
-                                 self.weight, self.weight_scale, stream)
+                                 self.weight, self.weight_scale)
             self.codes = torch.empty((T, self.H), dtype=torch.int8, device=dev)
             self.scale = torch.empty(T, dtype=torch.float32, device=dev)
             self.norm = None

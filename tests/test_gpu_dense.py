@@ -851,6 +851,37 @@ def test_token_head_behind_a_stack(bits, T):
     stack.close()
 
 
+@pytest.mark.parametrize("bits,dtype", [(8, torch.float32), (16, torch.float32), (16, torch.bfloat16)])
+@pytest.mark.parametrize("handle", ["stream", "address", "default"])
+def test_token_head_built_on_another_stream(bits, dtype, handle):
+    """The current stream is busy, with the weights' own values among its work; the head is built and used on
+    another without a wait between, and the weights are dropped at once."""
+    rs = np.random.default_rng(60 + bits)
+    V, H, T = 5003, 512, 3
+    values = rs.standard_normal((V, H)).astype(np.float32)
+    x, u = dev(rs.standard_normal((T, H)).astype(np.float32)), dev(uniforms(rs, T))
+    want = TokenHead(dev(values, dtype), T, bits=bits)
+    want.step(x, u)
+    torch.cuda.synchronize()
+    source = dev(values, dtype)
+    side = torch.cuda.default_stream() if handle == "default" else torch.cuda.Stream()
+    busy = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(busy):
+            weight = torch.full_like(source, 3.0)
+            torch.cuda._sleep(20_000_000)
+            weight.copy_(source)
+            head = TokenHead(weight, T, bits=bits, stream=side.cuda_stream if handle == "address" else side)
+            del weight
+            junk = [torch.full_like(source, 7.0) for _ in range(3)]   # takes the weights' memory over
+        head.step(x, u, stream=side)
+        torch.cuda.synchronize()
+        assert head.status() == 0
+        assert torch.equal(head.logits, want.logits) and torch.equal(head.token, want.token)
+        del head, junk
+
+
 def test_token_head_refusals():
     w = torch.zeros((100, 64), device="cuda")
     for bad in (dict(weight=w[0]), dict(weight=w.double()), dict(weight=w, bits=4), dict(weight=w, T=0),
