@@ -424,8 +424,8 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
         else tc05::commit(&b->fin);
       }
       __syncwarp();
+      if (!mbar_wait(&b->fin, 0, clock64() + WAIT_BUDGET_CYCLES)) set_status(a.status, DEV_TIMEOUT);
     }
-    if (!mbar_wait(&b->fin, 0, clock64() + WAIT_BUDGET_CYCLES * (PAIRS && rank ? 2 : 1))) set_status(a.status, DEV_TIMEOUT);
   } else if (warp >= LN_W_EPI && (PAIRS || a.split == 1)) {
     const int w = warp - LN_W_EPI, q = warp & 3, part = w >> 2;   // (a warp reads the TMEM lanes of its number mod 4)
     const int col0 = BT < 32 ? 0 : part * EPI_COLS;
@@ -697,6 +697,11 @@ __global__ void __launch_bounds__(ln_threads(MODE, BT), 1) linear_kernel(const _
 
   tc05::fence_before_sync();
   __syncthreads();
+  // The pair's other CTA issues no products: it waits for the end of theirs only now, when its
+  // epilogue has read the last of them (from the kernel's start the wait would span the whole
+  // kernel, and one that works for longer than a wait's budget would be taken for a hang).
+  if (PAIRS && rank && warp == LN_W_MMA && !mbar_wait(&b->fin, 0, clock64() + 2 * WAIT_BUDGET_CYCLES))
+    set_status(a.status, DEV_TIMEOUT);
   if (PAIRS) dense::cluster_sync();   // neither CTA's memory is in use by the other any more
   if (warp == LN_W_MMA) {
     tc05::fence_after_sync();

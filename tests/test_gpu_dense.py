@@ -344,6 +344,33 @@ def test_linear_full_size_chunk():
         assert q.qmoe_read_status(st) == 0
 
 
+def test_linear_that_takes_seconds():
+    """The longest rows by 200000 x 200000 results: more than 4e9 SM cycles in one launch, which is no reason for
+    a timeout. (1.2e6 products and sums a cycle at most on 148 SMs; both operands are the same matrix.)"""
+    M, K = 200_000, 65536
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 125 << 30:
+        pytest.skip("needs 106 GB")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    a = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, M, 20_000):
+        a[i:i + 20_000].normal_(generator=g)
+    out, st = torch.empty((M, M), dtype=torch.bfloat16, device="cuda"), status_word()
+    q.qmoe_linear(a, q.BF16, a, M, M, K, None, None, None, q.ACT_NONE, None, out, q.BF16, st)
+    torch.cuda.synchronize()
+    assert q.qmoe_read_status(st) == 0
+    rows = torch.tensor([0, 77, 128, 100_001, M - 1], device="cuda")
+    cols = torch.cat([rows, torch.randint(0, M, (100,), generator=g, device="cuda")])
+    x, y = a[rows].double(), a[cols].double()
+    want, mag = x @ y.T, x.abs() @ y.abs().T
+    tol = (K / 16 + 2) * 2 * U * mag
+    tol = tol + BF * (want.abs() + tol)
+    assert ((out[rows][:, cols].double() - want).abs() <= tol).all()
+    del a, out
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ sample --
 def run_sample(logits, dtype=q.F32, ld=0, V=None, temperature=None, top_k=None, top_p=None, min_p=None, u=None, st=None):
     T = logits.shape[0]
