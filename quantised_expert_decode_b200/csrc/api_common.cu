@@ -27,11 +27,10 @@ size_t max_smem_optin() {
 
 namespace dense {
 
-int max_clusters(int size, const void *fn, int threads, int smem) {
-  static std::atomic<int> known[16][MAX_CLUSTER + 1];
+int max_clusters(ClusterCounts &known, int size, const void *fn, int threads, int smem) {
   int dev = 0;
   if (size < 1 || size > MAX_CLUSTER || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return 0;
-  int n = known[dev][size].load(std::memory_order_relaxed);
+  int n = known.n[dev][size].load(std::memory_order_relaxed);
   if (n == 0) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(size);
@@ -48,7 +47,7 @@ int max_clusters(int size, const void *fn, int threads, int smem) {
       cudaGetLastError();
       return 0;
     }
-    known[dev][size].store(n, std::memory_order_relaxed);
+    known.n[dev][size].store(n, std::memory_order_relaxed);
   }
   return n;
 }

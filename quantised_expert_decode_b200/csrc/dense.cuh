@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace qmoe {
@@ -14,12 +16,16 @@ constexpr int32_t DEV_BAD_PARAM = 5;   // a per-row parameter read on the device
 
 namespace dense {
 
-// Clusters of `size` CTAs that run at once on the current device, for kernels whose
-// CTAs take an SM each, as `fn` with these threads and shared memory does (a cluster lies within one part of
-// the chip: 16 clusters of 8 do not fit on 148 SMs, and a second wave costs more than
-// fewer CTAs). 0 where that cannot be told.
+// Clusters of `size` CTAs of `fn`, with these threads and shared memory, that run at once on
+// the current device (a cluster lies within one part of the chip: 16 clusters of 8 CTAs
+// that take an SM each do not fit on 148 SMs, and a second wave costs more than
+// fewer CTAs). 0 where that cannot be told. Kept in the caller's own table, one for each
+// kernel: what one kernel's calls find decides nothing for another's.
 constexpr int MAX_CLUSTER = 8;
-int max_clusters(int size, const void *fn, int threads, int smem);
+struct ClusterCounts {
+  std::atomic<int> n[16][MAX_CLUSTER + 1];   // device, size
+};
+int max_clusters(ClusterCounts &known, int size, const void *fn, int threads, int smem);
 
 // The status of a call that launched nothing more: a refused launch leaves no error
 // behind that a later call would take for its own.

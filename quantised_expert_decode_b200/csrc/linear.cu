@@ -31,8 +31,6 @@
 // steps only, and the epilogue's threads add the slots' values with rounding.
 #include <cuda_bf16.h>
 
-#include <atomic>
-
 #include "dense.cuh"
 #include "tc05.cuh"
 
@@ -738,7 +736,8 @@ const void *ln_kernel(bool i8, bool f32) {
 }
 
 int ln_max_clusters(int size) {
-  return dense::max_clusters(size, (const void *)linear_kernel<LN_FEATURES, 16, true, false>, ln_threads(LN_FEATURES, 16),
+  static dense::ClusterCounts known;   // (of one kernel that stands for all that split K: they take an SM a CTA)
+  return dense::max_clusters(known, size, (const void *)linear_kernel<LN_FEATURES, 16, true, false>, ln_threads(LN_FEATURES, 16),
                              ln_smem_bytes(LN_FEATURES, 16));
 }
 

@@ -1472,10 +1472,11 @@ extern "C" qmoe_status qmoe_sample(const void *logits, int dtype, int T, int V, 
   // out of L2 (40 rows 50 us, in shared memory in turns 75; 73 rows 67 and 124), and at
   // least two per row where the rows under way do not fit there (256 rows of 131072:
   // 139 us, one each 148; of 60000: one each 72 us, two 82).
+  static dense::ClusterCounts known[2];   // by type
   const int sms = num_sms();
   int nc = SP_MAX_CLUSTER;
   while (nc > 1 && (V < nc * SP_MIN_SLICE || T * (long long)nc > sms ||
-                    T > dense::max_clusters(nc, kernel(true), SP_THREADS, smem_of(true, SP_MAX_SLICE / SP_WARPS))))
+                    T > dense::max_clusters(known[dtype == QMOE_BF16], nc, kernel(true), SP_THREADS, smem_of(true, SP_MAX_SLICE / SP_WARPS))))
     nc /= 2;
   const bool res = T <= sms && (V + nc - 1) / nc <= SP_MAX_SLICE;
   if (!res) {

@@ -14,6 +14,9 @@ Tolerances (u = 2^-24, half an fp32 step relative to the value):
   most 1.13 and are formed to 2e-6 of |v|.
 """
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -733,6 +736,33 @@ def test_two_host_threads_with_calls_of_different_sizes(op):
     for (_, _, out, value), (o, v) in zip(keep, want):
         assert torch.equal(out, o) and torch.equal(value, v)
     assert q.qmoe_read_status(st) == 0
+
+
+ORDER = """
+import hashlib, sys, torch
+import quantised_expert_decode_b200 as q
+g = torch.Generator(device="cuda")
+g.manual_seed(3)
+st = torch.zeros(1, dtype=torch.int32, device="cuda")
+a, w = (torch.randn(r, 2048, generator=g, device="cuda").bfloat16() for r in (5, 2048))
+logits, u = torch.randn(18, 131072, generator=g, device="cuda"), torch.rand(18, generator=g, device="cuda")
+out, token, prob = torch.empty(5, 2048, device="cuda"), torch.empty(18, dtype=torch.int32, device="cuda"), torch.empty(18, device="cuda")
+for op in sys.argv[1]:
+    if op == "p":
+        q.qmoe_linear(a, q.BF16, w, 5, 2048, 2048, None, None, None, q.ACT_NONE, None, out, q.F32, st)
+    else:
+        q.qmoe_sample(logits, q.F32, 18, 131072, None, None, u, None, u, token, prob, st)
+assert q.qmoe_read_status(st) == 0
+print(hashlib.sha256(b"".join(t.cpu().numpy().tobytes() for t in (out, token, prob))).hexdigest())
+"""
+
+
+def test_results_do_not_depend_on_which_operator_ran_first():
+    """How a call is spread over the chip is not decided by another operator's earlier calls."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = [subprocess.run([sys.executable, "-c", ORDER, order], cwd=root, capture_output=True, text=True, timeout=300, check=True).stdout
+           for order in ("ps", "sp")]
+    assert got[0] == got[1] and len(got[0].strip()) == 64
 
 
 @pytest.mark.parametrize("T,H", [(1, 256), (70, 512), (600, 2048)])
