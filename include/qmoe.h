@@ -387,7 +387,8 @@ qmoe_status qmoe_ngram_gather(const int32_t *ngrams, int T, uint64_t seed, const
  *   z = x_in[t,:] + y[t,:]                  (fp32, one rounding; y NULL: z = x_in)
  *   r = 1 / sqrt(mean(z^2) + eps),  p = z * gain    (gain NULL: p = z)
  *   z_out    = z in `dtype`                 (the updated residual stream)
- *   norm_out = p * r in bf16
+ *   norm_out = p * r in bf16                (of the sum before z_out's rounding: with a bf16 stream not
+ *                                            the norm of the row that z_out holds)
  *   codes    = rint(127 p / A), ties to even;  scales = A r / 127 in fp32
  *   A        = max |p| over the scale's columns
  * The code c stands for c * scale. group 0: one scale per row, scales [T];
@@ -395,7 +396,8 @@ qmoe_status qmoe_ngram_gather(const int32_t *ngrams, int T, uint64_t seed, const
  * Codes are exact: bit for bit those of float64 arithmetic on the fp32 z, as
  * rint((z * gain) * 127 / A); no rounding error of a sum enters them. All zero
  * columns give codes 0 and scale 0. A NaN or infinity in z makes the row's
- * scales and norm_out NaN and its codes 0 (in gain: those of its groups).
+ * scales and norm_out NaN and its codes 0 (in gain: those of its groups). Beside
+ * codes, a column whose |p| is below 2^-126 has up to 2^-150 r of error in norm_out.
  * x_in, y, z_out: [T,H] of dtype QMOE_F32 or QMOE_BF16; gain fp32 [H];
  * norm_out bf16 [T,H]; codes int8 [T,H]. y, gain, z_out, norm_out may be NULL,
  * and codes with scales; codes or norm_out must be there. z_out may alias x_in

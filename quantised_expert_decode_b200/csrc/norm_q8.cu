@@ -333,6 +333,21 @@ __global__ void __launch_bounds__(NQ_MAX_THREADS, 2) norm_q8_kernel(const __grid
       const size_t e = row + (size_t)ch * NQ_VEC;
       float p[NQ_VEC];
       nq_get(zs, live ? ch : 0, p);
+      if (NORM && !a.codes) {
+        // the normed row alone: (z r) gain, as |z r| is at most sqrt(H), while z gain may leave
+        // the fp32 range where the normed row does not
+#pragma unroll
+        for (int i = 0; i < NQ_VEC; ++i) p[i] = __fmul_rn(p[i], inv);
+        if (gain) {
+          float g[NQ_VEC];
+          nq_load<false>(a.gain, (size_t)(live ? ch : 0) * NQ_VEC, g);
+#pragma unroll
+          for (int i = 0; i < NQ_VEC; ++i) p[i] = __fmul_rn(p[i], g[i]);
+        }
+        const uint4 o = nq_bf16x8(p);
+        if (live) *reinterpret_cast<uint4 *>(a.norm + e) = o;
+        continue;
+      }
       if (gain) {
         float g[NQ_VEC];
         nq_load<false>(a.gain, (size_t)(live ? ch : 0) * NQ_VEC, g);
@@ -340,13 +355,14 @@ __global__ void __launch_bounds__(NQ_MAX_THREADS, 2) norm_q8_kernel(const __grid
         for (int i = 0; i < NQ_VEC; ++i) p[i] = __fmul_rn(p[i], g[i]);
       }
       if (NORM && a.norm) {
+        // (z gain) r, as the codes need z gain: the columns whose largest product leaves the range
+        // below are done again; a product below 2^-126 among larger ones is off by up to 2^-150
         float v[NQ_VEC];
 #pragma unroll
         for (int i = 0; i < NQ_VEC; ++i) v[i] = __fmul_rn(p[i], inv);
         const uint4 o = nq_bf16x8(v);
         if (live) *reinterpret_cast<uint4 *>(a.norm + e) = o;
       }
-      if (!a.codes) continue;
 
       if (a.group != 0) {
         uint32_t m = 0;

@@ -131,6 +131,31 @@ def test_norm_extreme_rows(group):
     assert np.array_equal(to_np(codes), co) and np.array_equal(np.isnan(to_np(scales)), np.isnan(so))
 
 
+@pytest.mark.parametrize("T", [3, 700])
+@pytest.mark.parametrize("size,gains", [(1e10, 1e30), (1e-10, 1e-32), (1.0, 1e37), (1e10, None), (1e-11, None)])
+@pytest.mark.parametrize("group", [None, 0, 64])
+def test_norm_rows_of_gains_far_from_one(T, size, gains, group):
+    """z times gain leaves the fp32 range although the normed row does not; with codes and without."""
+    H = 576
+    rs = np.random.default_rng(T)
+    x = (size * rs.standard_normal((T, H))).astype(np.float32)
+    # (None: gains of many sizes side by side)
+    gain = (np.exp2(rs.integers(-100, 110, H)) if gains is None else gains * (0.5 + rs.random(H))).astype(np.float32)
+    xd, gd = dev(x), dev(gain)
+    z, no, co, so = dense.norm_q8(x, None, gain, 1e-30, group or 0)
+    _, norm, codes, scales = run_norm(xd, None, q.F32, gd, group or 0, eps=1e-30, want_codes=group is not None)
+    n = f64(norm)
+    # with codes z gain is rounded first: where it lies below 2^-126, to a multiple of 2^-149, so that r times half
+    # of that adds to the error
+    r = 1 / np.sqrt((x.astype(np.float64) ** 2).mean(1, keepdims=True) + 1e-30)
+    tol = (BF + 41 * U) * np.abs(no) + 1e-40 + (0 if group is None else 2.0 ** -150 * r)
+    fine = np.abs(no) < 3e38
+    assert (np.abs(n - no) <= tol)[fine].all()
+    if group is not None:
+        assert np.array_equal(to_np(codes), co)
+        assert (np.abs(f64(scales) - so) <= 40 * U * so + 1e-45).all()
+
+
 @pytest.mark.parametrize("T,H,group", [(2500, 272, 0), (2500, 1056, 32), (700, 4112, 0), (700, 5248, 64), (149, 2048, 128)])
 @pytest.mark.parametrize("dtype", [q.F32, q.BF16])
 def test_norm_many_rows(T, H, group, dtype):
