@@ -423,7 +423,8 @@ qmoe_status qmoe_quantise_rows(const void *x, int dtype, int T, int H, int group
  *   in_dtype QMOE_I8: a, w int8, exact int32 accumulators, a_scale fp32 [M] and
  *     w_scale fp32 [N]: the codes and row scales of the calls above.
  *   out_dtype QMOE_F32 or QMOE_BF16, of out and residual (fp32 arithmetic, one
- *     rounding); bias fp32 [N] or NULL; residual [M,N] or NULL, may be out.
+ *     rounding); bias fp32 [N] or NULL; residual [M,N] or NULL, may be out
+ *     (with ldr = ldo; else it must not overlap out).
  *   act QMOE_ACT_NONE, _RELU, _SILU (v / (1 + exp(-v))), _GELU (v Phi(v)).
  *   lda, ldw, ldr, ldo: row strides in elements, 0 = packed (K, K, N, N).
  *     Columns past K (or N) of a row are neither read nor written.
@@ -431,9 +432,10 @@ qmoe_status qmoe_quantise_rows(const void *x, int dtype, int T, int H, int group
  * Limits: 1 <= M, N <= 2^30, 1 <= K <= 65,536; rows of a and w must start on 16 bytes
  * (lda, ldw multiples of 8 for bf16, of 16 for int8). Alignment: 16 bytes.
  * out must not overlap a, w, the scales or bias. Errors: INVALID_ARG (null or
- * misaligned pointers, strides below the row, scales missing or not wanted),
- * UNSUPPORTED (M, N, K, row alignment, strides above 2^37); device status TIMEOUT if a wait inside the
- * kernel ran out of its budget. */
+ * misaligned pointers, strides below the row, scales missing or not wanted,
+ * residual = out at another stride), UNSUPPORTED (M, N, K, row alignment, strides
+ * above 2^37); device status TIMEOUT if a wait inside the kernel ran out of its
+ * budget (about a second without progress). */
 qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, int M, int N, int K, const float *a_scale,
                         const float *w_scale, const float *bias, int act, const void *residual, void *out,
                         int out_dtype, int64_t lda, int64_t ldw, int64_t ldr, int64_t ldo, int32_t *dev_status,

@@ -776,6 +776,8 @@ extern "C" qmoe_status qmoe_linear(const void *a, int in_dtype, const void *w, i
   // rows of a and w start on 16 bytes (the copy engine's rule); strides below 2^40 bytes
   if (lda > LN_MAX_LD || ldw > LN_MAX_LD || ldo > LN_MAX_LD || (residual && ldr > LN_MAX_LD)) return QMOE_ERR_UNSUPPORTED;
   if (lda * es % 16 || ldw * es % 16 || K > LN_MAX_K || M > LN_MAX_MN || N > LN_MAX_MN) return QMOE_ERR_UNSUPPORTED;
+  // a residual that is overwritten in place: row by row, or results would be read as residuals
+  if (residual == out && ldr != ldo && M > 1) return QMOE_ERR_INVALID_ARG;
   LnArgs g{};
   g.s_a = a_scale;
   g.s_w = w_scale;

@@ -91,6 +91,16 @@ def test_linear_strides_past_the_limit_are_refused():
         assert call(**{name: big}) == 3 and call(**{name: (1 << 37) + 8}) == 3, name
 
 
+def test_linear_in_place_at_another_stride_is_refused():
+    lib, F = q.lib(), FAKE
+
+    def call(M, ldr, ldo, out):
+        return lib.qmoe_linear(F, q.BF16, F, M, 8, 8, None, None, None, 0, F, out, q.F32, 0, 0, ldr, ldo, F, None)
+
+    for ldr, ldo in ((16, 8), (0, 12), (8, 16)):
+        assert call(2, ldr, ldo, F) == 1
+
+
 @pytest.mark.gpu
 def test_binding_refuses_a_status_word_off_the_device():
     torch = pytest.importorskip("torch")
