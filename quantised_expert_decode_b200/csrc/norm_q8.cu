@@ -14,9 +14,9 @@
 //
 // Bound: HBM bandwidth for fp32 rows (one read of x and y, one write per output; z
 // waits in shared memory between the statistics and the codes: 8192 x 2048 with
-// x, y and z in fp32 41.1 us, 81 % of the measured copy rate), for bf16 rows the
-// issue of some 40 instructions a column (8192 x 2048 with the normed rows too 33.5 us,
-// 69 %). One CTA per row at a time, 8 neighbouring columns per thread and round, CTAs
+// x, y and z in fp32 41.4 us, 80 % of the measured copy rate), for bf16 rows the
+// issue of some 40 instructions a column (8192 x 2048 with the normed rows too 34.3 us,
+// 67 %). One CTA per row at a time, 8 neighbouring columns per thread and round, CTAs
 // loop over rows, two rows' z in turn, so that one CTA barrier per row carries all
 // statistics; the next row is fetched into L2 meanwhile. What is rare follows the
 // loop as loops of its own: called, or inlined where it is found, it took registers

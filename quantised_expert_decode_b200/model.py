@@ -109,8 +109,9 @@ class DecodeStack:
 class TokenHead:
     """What follows a layer stack: final RMSNorm -> vocabulary product -> sampled tokens, three kernels.
 
-    ``weight`` bf16 or fp32 [V, H]. With ``bits`` 8 its rows are kept as int8 codes and fp32 scales
-    (qmoe_quantise_rows) and the normed rows are 8-bit too; with ``bits`` 16 both are bf16. ``gain`` fp32 [H]
+    ``weight`` bf16 or fp32 [V, H]. With ``bits`` 8, the default, its rows are kept as int8 codes and fp32 scales
+    (qmoe_quantise_rows) and the normed rows are rounded to 8 bits too, which halves the bytes of a step but is
+    coarser than weights given in 16 bits or more; with ``bits`` 16 both are bf16. ``gain`` fp32 [H]
     or None; ``bias`` fp32 [V] or None. All buffers are made here, on ``stream`` where one is given; ``step`` only
     launches, and can be captured. Two steps that overlap on different streams need a head each.
     """
@@ -178,4 +179,6 @@ class TokenHead:
         return self.token
 
     def status(self) -> int:
+        """The first error of all steps so far, 0 if there was none (waits for the device). A row out of range stays
+        reported until ``dev_status.zero_()``."""
         return L.qmoe_read_status(self.dev_status)
