@@ -597,9 +597,10 @@ __device__ __forceinline__ void push_all(T *at, const T &v, int nc) {
   if (lane < nc) *dense::peer(at, lane) = v;
 }
 
-// Ascending keys are ascending ranks: logit descending, then index.
+// Ascending keys are ascending ranks: logit descending, then index. (-0 + 0 is 0: zeros
+// of either sign are one logit.)
 __device__ __forceinline__ unsigned long long sq_key(float l, int i) {
-  return ((unsigned long long)~float_key(l) << 32) | (unsigned)i;
+  return ((unsigned long long)~float_key(__fadd_rn(l, 0.0f)) << 32) | (unsigned)i;
 }
 __device__ __forceinline__ float sq_key_logit(unsigned long long k) { return key_float(~(unsigned)(k >> 32)); }
 

@@ -488,6 +488,22 @@ def test_sample_ties():
     check_sample(bf, q.BF16, u=uniforms(rs, 4), top_k=[3, 600, 60000, 131071])
 
 
+@pytest.mark.parametrize("T,V", [(6, 700), (6, 40000), (170, 3000)])
+@pytest.mark.parametrize("dtype", [q.F32, q.BF16])
+def test_sample_zeros_of_either_sign_are_equal(T, V, dtype):
+    """-0 and 0 are one logit: the lower index ranks first, whichever sign it has."""
+    rs = np.random.default_rng(V + dtype)
+    l = np.where(rs.random((T, V)) < 0.5, np.float32(0.0), np.float32(-0.0))
+    l[rs.random((T, V)) < 0.95] = -40.0
+    l[1::3] = np.round(1.2 * rs.standard_normal((len(l[1::3]), V)))       # values -4 .. 4, with zeros of either sign
+    l[2::3, V // 3] = 0.25
+    u = uniforms(rs, T)
+    check_sample(l, dtype, u=u, top_k=rs.integers(2, 30, T))
+    check_sample(l, dtype, u=u, top_p=0.2 + 0.6 * rs.random(T))
+    check_sample(l, dtype, u=u, top_k=rs.integers(2, 600, T), top_p=0.3 + 0.7 * rs.random(T), min_p=np.full(T, 0.01))
+    check_sample(l, dtype, u=u, temperature=np.zeros(T))
+
+
 def test_sample_empty_rows_and_infinities():
     l = np.full((5, 300), -np.inf, dtype=np.float32)
     l[1, 7] = np.nan
